@@ -13,6 +13,8 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libckda.so"
 
 CKDA_F32 = 0
 CKDA_BF16 = 1
+CKDA_NORM_L2 = 0
+CKDA_NORM_RMS = 1
 # capacity of the library's static device scratch (ckda_fwd_chunked_static)
 CKDA_STATIC_SCRATCH_BYTES = 64 * 1024 * 1024
 
@@ -55,6 +57,17 @@ SIGNATURES = {
     "ckda_gdn2_decode_step": (_i, [_vp] * 8 + [_i] * 6 + [_vp]),
     "ckda_sfda_decode_step": (_i, [_vp] * 8 + [_i] * 6 + [_vp]),
     "ckda_decode_step": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp]),
+    "ckda_la_fwd_chunked": (_i, [_vp] * 8 + [_i] * 8 + [_vp, ctypes.c_size_t, _vp]),
+    "ckda_la_fwd_workspace_bytes": (ctypes.c_int64, [_i] * 7),
+    "ckda_la_bwd_chunked": (_i, [_vp] * 13 + [_i] * 7 + [_vp, ctypes.c_size_t, _vp]),
+    "ckda_la_bwd_workspace_bytes": (ctypes.c_int64, [_i] * 8),
+    "ckda_la_decode_step": (_i, [_vp] * 6 + [_i] * 7 + [_vp]),
+    "ckda_qk_norm_rope": (_i, [_vp] * 8 + [ctypes.c_int64] + [_i] * 6
+                          + [ctypes.c_float, ctypes.c_int64, ctypes.c_int64, _i, _i, _vp]),
+    "ckda_qk_norm_rope_bwd": (_i, [_vp] * 12 + [ctypes.c_int64] + [_i] * 6
+                              + [ctypes.c_float, ctypes.c_int64, ctypes.c_int64, _i, _vp,
+                                 ctypes.c_size_t, _vp]),
+    "ckda_qk_norm_rope_bwd_workspace_bytes": (ctypes.c_int64, [_i]),
     "ckda_status_string": (ctypes.c_char_p, [_i]),
     "ckda_device_status": (_i, [_vp]),
     "ckda_selftest_bounded_wait": (_i, [_i, _vp]),

@@ -543,6 +543,309 @@ def sfda_decode_step(q, k, v, alpha, theta, beta, S, out=None, out_dtype=None) -
     return out
 
 
+# ---- head-decay linear attention ------------------------------------------------
+
+
+def _la_inputs(q, k, v, alpha, cu_seqlens):
+    """Checks the inputs; returns (B, T, H, dk, dv, per_head) as passed to the ABI."""
+    dev = q.device
+    if q.dtype not in _DT:
+        raise TypeError("q, k, v must be float32 or bfloat16")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _need(t, name, q.dtype, dev)
+    _need(alpha, "alpha", torch.float32, dev)
+    if cu_seqlens is None:
+        if q.dim() != 4:
+            raise ValueError("q must be [B, T, H, dk]")
+        B, T, H, dk = q.shape
+    else:
+        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be [N + 1]")
+        if q.dim() == 4:
+            if q.shape[0] != 1:
+                raise ValueError("packed inputs take a leading dimension of 1")
+        elif q.dim() != 3:
+            raise ValueError("q must be [T, H, dk] or [1, T, H, dk]")
+        T, H, dk = q.shape[-3:]
+        B = cu_seqlens.numel() - 1
+    if k.shape != q.shape or v.dim() != q.dim() or v.shape[:-1] != q.shape[:-1]:
+        raise ValueError("q and k must share a shape and v must match it but for the last dim")
+    per_head = alpha.dim() == 1
+    if alpha.shape != ((H,) if per_head else q.shape[:-1]):
+        raise ValueError("alpha must have q's shape without the last dim, or be [H]")
+    return B, T, H, dk, v.shape[-1], per_head
+
+
+def _la_state(t, name, shape, dev):
+    if t is not None:
+        _need(t, name, torch.float32, dev)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}")
+
+
+def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, varlen=False) -> int:
+    """Scratch bytes ``la_fwd_chunked`` needs for these sizes."""
+    rc = _lib.load().ckda_la_fwd_workspace_bytes(B, T, H, dk, dv, _DT[dtype], 1 if varlen else 0)
+    if rc < 0:
+        raise CKDAError(int(rc), "ckda_la_fwd_workspace_bytes")
+    return int(rc)
+
+
+def la_fwd_chunked(q, k, v, alpha, S0=None, cu_seqlens=None, out=None, S_final=None,
+                   return_final: bool = True, out_dtype=None, workspace=None):
+    """Chunked forward of head-decay linear attention (``ckda_la_fwd_chunked``):
+    ``S_t = a_t S_{t-1} + k_t v_t^T``, ``o_t = S_t^T q_t``.
+
+    q, k ``[B, T, H, dk]``, v ``[B, T, H, dv]``, alpha (fp32) ``[B, T, H]``, or ``[H]``
+    for one decay per head; packed batches as in ``fwd_chunked``, and so the other
+    arguments.  Returns ``(out, S_final)``."""
+    dev = q.device
+    B, T, H, dk, dv, per_head = _la_inputs(q, k, v, alpha, cu_seqlens)
+    _la_state(S0, "S0", (B, H, dk, dv), dev)
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else q.dtype
+    if out_dtype not in _DT:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    if out is None:
+        out = torch.empty(v.shape, dtype=out_dtype, device=dev)
+    else:
+        _need(out, "out", out_dtype, dev)
+        if out.shape != v.shape:
+            raise ValueError("out must have v's shape")
+    if return_final and S_final is None:
+        S_final = torch.empty((B, H, dk, dv), dtype=torch.float32, device=dev)
+    else:
+        _la_state(S_final, "S_final", (B, H, dk, dv), dev)
+    need = la_workspace_bytes(B, T, H, dk, dv, q.dtype, cu_seqlens is not None)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        rc = _lib.load().ckda_la_fwd_chunked(
+            _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(out), _p(S_final), B, T, H,
+            dk, dv, 1 if per_head else 0, _DT[q.dtype], _DT[out_dtype], _p(workspace),
+            0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+    if rc != 0:
+        raise CKDAError(rc, "ckda_la_fwd_chunked")
+    return out, S_final
+
+
+def la_bwd_workspace_bytes(B, T, H, dk, dv, alpha_per_head=False, dtype=torch.bfloat16,
+                           varlen=False) -> int:
+    """Scratch bytes ``la_bwd_chunked`` needs for these sizes."""
+    rc = _lib.load().ckda_la_bwd_workspace_bytes(B, T, H, dk, dv, 1 if alpha_per_head else 0,
+                                                 _DT[dtype], 1 if varlen else 0)
+    if rc < 0:
+        raise CKDAError(int(rc), "ckda_la_bwd_workspace_bytes")
+    return int(rc)
+
+
+def la_bwd_chunked(q, k, v, alpha, dO, S0=None, dS_final=None, cu_seqlens=None, grads=None,
+                   want_dS0: bool = True, workspace=None):
+    """Backward of ``la_fwd_chunked`` (``ckda_la_bwd_chunked``) given ``dO`` (dL/dout, shaped
+    and typed like v) and ``dS_final`` (dL/dS_final, fp32, or None = 0).
+
+    Returns a dict: ``dq, dk, dv`` shaped and typed like the inputs, ``dalpha`` (fp32, shaped
+    like alpha) and ``dS0`` (fp32 ``[N, H, dk, dv]``, or None when ``want_dS0`` is false).
+    ``grads`` may supply preallocated output tensors under the same names."""
+    dev = q.device
+    B, T, H, dk, dv, per_head = _la_inputs(q, k, v, alpha, cu_seqlens)
+    _need(dO, "dO", q.dtype, dev)
+    if dO.shape != v.shape:
+        raise ValueError("dO must have v's shape")
+    st = (B, H, dk, dv)
+    _la_state(S0, "S0", st, dev)
+    _la_state(dS_final, "dS_final", st, dev)
+    want = [("dq", q.shape, q.dtype), ("dk", k.shape, q.dtype), ("dv", v.shape, q.dtype),
+            ("dalpha", alpha.shape, torch.float32)]
+    if want_dS0:
+        want.append(("dS0", st, torch.float32))
+    g = {}
+    for name, shape, dtype in want:
+        t = (grads or {}).get(name)
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=dev)
+        else:
+            _need(t, name, dtype, dev)
+            if t.shape != shape:
+                raise ValueError(f"{name} must be {list(shape)}")
+        g[name] = t
+    if not want_dS0:
+        g["dS0"] = None
+    need = la_bwd_workspace_bytes(B, T, H, dk, dv, per_head, q.dtype, cu_seqlens is not None)
+    if workspace is None and need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        rc = _lib.load().ckda_la_bwd_chunked(
+            _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(dO), _p(dS_final),
+            _p(g["dq"]), _p(g["dk"]), _p(g["dv"]), _p(g["dalpha"]), _p(g["dS0"]), B, T, H, dk, dv,
+            1 if per_head else 0, _DT[q.dtype], _p(workspace),
+            0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+    if rc != 0:
+        raise CKDAError(rc, "ckda_la_bwd_chunked")
+    return g
+
+
+def la_decode_step(q, k, v, alpha, S, out=None, out_dtype=None) -> torch.Tensor:
+    """One token of head-decay linear attention in place on ``S`` ``[B, H, dk, dv]``
+    (``ckda_la_decode_step``): alpha (fp32) ``[B, H]``, or ``[H]`` for one decay per
+    head; otherwise as ``decode_step``."""
+    B, H, dk = q.shape
+    per_head = isinstance(alpha, torch.Tensor) and alpha.dim() == 1
+    dev, B, H, dk, dv = _decode_checks(q, k, v, S,
+                                       (("alpha", alpha, (H,) if per_head else (B, H)),))
+    out, out_dtype = _decode_out(q, v, out, out_dtype, dev)
+    if out.shape != v.shape:
+        raise ValueError("out must have v's shape")
+    with torch.cuda.device(dev):
+        rc = _lib.load().ckda_la_decode_step(
+            _p(q), _p(k), _p(v), _p(alpha), _p(S), _p(out), B, H, dk, dv, 1 if per_head else 0,
+            _DT[q.dtype], _DT[out_dtype], _stream_ptr(dev))
+    if rc != 0:
+        raise CKDAError(rc, "ckda_la_decode_step")
+    return out
+
+
+# ---- norm of queries and keys, with the rotation ----------------------------------
+
+_NORM = {"l2": _lib.CKDA_NORM_L2, "rms": _lib.CKDA_NORM_RMS}
+
+
+def _token_stride(t, name):
+    """Elements between the tokens of ``[..., H, d]``: the heads of a token lie together, the
+    tokens at one distance (a view into a wider projection)."""
+    H, d = t.shape[-2:]
+    if t.numel() == 0:
+        return H * d
+    if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != d):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    step, span = None, None
+    for n, s in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if step is None:
+            step, span = s, s * n
+        elif s != span:
+            raise ValueError(f"the tokens of {name} must lie at one stride")
+        else:
+            span = s * n
+    return H * d if step is None else step
+
+
+def _qk_inputs(q, k, wq, wk, positions, inv_freq, norm):
+    """Checks the inputs; returns (tokens, Hq, Hk, d, rot, q_stride, k_stride)."""
+    for name, t in (("q", q), ("k", k)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+    dev = q.device
+    if q.dtype not in _DT:
+        raise TypeError("q, k must be float32 or bfloat16")
+    if k.dtype != q.dtype or k.device != dev:
+        raise ValueError("q and k must share a dtype and a device")
+    if q.dim() < 3 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or \
+            k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must be [..., H, d] with the same tokens and d")
+    if norm not in _NORM:
+        raise ValueError("norm must be 'l2' or 'rms'")
+    lead, (Hq, d), Hk = q.shape[:-2], q.shape[-2:], k.shape[-2]
+    for name, w in (("wq", wq), ("wk", wk)):
+        if w is not None:
+            _need(w, name, torch.float32, dev)
+            if w.shape != (d,):
+                raise ValueError(f"{name} must be [{d}]")
+    rot = 0
+    if (positions is None) != (inv_freq is None):
+        raise ValueError("positions and inv_freq come together")
+    if positions is not None:
+        _need(positions, "positions", torch.int32, dev)
+        _need(inv_freq, "inv_freq", torch.float32, dev)
+        if positions.shape != lead or inv_freq.dim() != 1:
+            raise ValueError("positions must have the tokens' shape and inv_freq be [rot / 2]")
+        rot = 2 * inv_freq.numel()
+    return math.prod(lead), Hq, Hk, d, rot, _token_stride(q, "q"), _token_stride(k, "k")
+
+
+def qk_norm_rope(q, k, wq=None, wk=None, positions=None, inv_freq=None, norm: str = "rms",
+                 eps: float = 1e-6, interleaved: bool = False, q_out=None, k_out=None,
+                 out_dtype=None):
+    """Norm of every head of q and k and the rotation by position in one pass
+    (``ckda_qk_norm_rope``): the q and k that the recurrences of this package take.
+
+    q ``[..., Hq, d]`` and k ``[..., Hk, d]`` share the tokens' shape; they may be views
+    into one projection's output (the heads of a token contiguous, tokens at one stride).
+    ``norm`` "rms" (unit mean square) or "l2" (unit length), ``wq``, ``wk`` fp32 ``[d]`` or
+    None.  ``positions`` (int32, the tokens' shape) and ``inv_freq`` (fp32 ``[rot / 2]``)
+    turn the first ``rot`` channels: pairs ``(p, p + rot / 2)``, or ``(2p, 2p + 1)`` when
+    ``interleaved``; without them nothing is turned.  ``q_out`` and ``k_out`` may be q and k
+    themselves if those are contiguous.  Returns ``(q_out, k_out)``, contiguous."""
+    n, Hq, Hk, d, rot, qs, ks = _qk_inputs(q, k, wq, wk, positions, inv_freq, norm)
+    dev = q.device
+    if out_dtype is None:
+        out_dtype = q_out.dtype if q_out is not None else q.dtype
+    if out_dtype not in _DT:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    outs = []
+    for name, t, x in (("q_out", q_out, q), ("k_out", k_out, k)):
+        if t is None:
+            t = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        else:
+            _need(t, name, out_dtype, dev)
+            if t.shape != x.shape:
+                raise ValueError(f"{name} must have {name[0]}'s shape")
+        outs.append(t)
+    with torch.cuda.device(dev):
+        rc = _lib.load().ckda_qk_norm_rope(
+            _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(outs[0]), _p(outs[1]),
+            n, Hq, Hk, d, rot, 1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype],
+            _DT[out_dtype], _stream_ptr(dev))
+    if rc != 0:
+        raise CKDAError(rc, "ckda_qk_norm_rope")
+    return outs[0], outs[1]
+
+
+def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, inv_freq=None,
+                     norm: str = "rms", eps: float = 1e-6, interleaved: bool = False,
+                     workspace=None):
+    """Backward of ``qk_norm_rope`` (``ckda_qk_norm_rope_bwd``) given ``dq_out`` and
+    ``dk_out`` (contiguous, q's dtype); the other arguments are those of the forward.
+
+    Returns a dict: ``dq``, ``dk`` (contiguous, q's dtype) and ``dwq``, ``dwk`` (fp32
+    ``[d]``, each None without its weight)."""
+    n, Hq, Hk, d, rot, qs, ks = _qk_inputs(q, k, wq, wk, positions, inv_freq, norm)
+    dev = q.device
+    for name, t, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
+        _need(t, name, q.dtype, dev)
+        if t.shape != x.shape:
+            raise ValueError(f"{name} must have {name[1]}'s shape")
+    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
+         "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
+         "dwq": None if wq is None else torch.empty(d, dtype=torch.float32, device=dev),
+         "dwk": None if wk is None else torch.empty(d, dtype=torch.float32, device=dev)}
+    lib = _lib.load()
+    if workspace is None and (wq is not None or wk is not None):
+        need = lib.ckda_qk_norm_rope_bwd_workspace_bytes(d)
+        if need < 0:
+            raise CKDAError(int(need), "ckda_qk_norm_rope_bwd_workspace_bytes")
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if workspace is not None:
+        _need(workspace, "workspace", torch.uint8, dev)
+    with torch.cuda.device(dev):
+        rc = lib.ckda_qk_norm_rope_bwd(
+            _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(dq_out), _p(dk_out),
+            _p(g["dq"]), _p(g["dk"]), _p(g["dwq"]), _p(g["dwk"]), n, Hq, Hk, d, rot,
+            1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype], _p(workspace),
+            0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+    if rc != 0:
+        raise CKDAError(rc, "ckda_qk_norm_rope_bwd")
+    return g
+
+
 def device_status(device=None) -> int:
     """Synchronise the current stream and return (and clear) the device status word."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)

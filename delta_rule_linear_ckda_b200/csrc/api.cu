@@ -70,6 +70,15 @@ int* status_ptr() {
   return p;
 }
 
+}  // namespace
+
+namespace ckda {
+// for the entry points in la_api.cu
+int* status_word() { return status_ptr(); }
+}  // namespace ckda
+
+namespace {
+
 std::atomic<void*> g_scratch_ptr[kMaxDevices];
 
 // Device address of the static scratch on the current device, looked up

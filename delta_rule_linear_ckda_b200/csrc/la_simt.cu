@@ -1,0 +1,512 @@
+// Head-decay linear attention on fp32 CUDA cores: every head size and type
+// that the tensor-core kernels do not take.
+//
+// Forward, token by token: S_t = a_t S_{t-1} + k_t v_t^T, o_t = S_t^T q_t.
+// With G_t the adjoint of S_t (G_t = q_t do_t^T + a_{t+1} G_{t+1}) the
+// gradients are the same recurrence with other operands:
+//   dq_t = S_t do_t    queries do, keys v, values k  (state S^T, forward in time)
+//   dk_t = G_t v_t     queries v, keys do, values q  (state G^T, backward in time)
+//   dv_t = G_t^T k_t   queries k, keys q, values do  (state G, backward in time)
+// so one kernel runs all four.  The decay's gradient da_t = <S_{t-1}, G_t>
+// is put together chunk by chunk from the states at the chunk's bounds,
+// which the dq and dv runs leave behind (la_dalpha_kernel).
+//
+// A recurrence costs 3 d_k d_v fp32 operations per token (the decay and the
+// outer product, the product with the queries): as many as the chunked form
+// with 64-token chunks needs without tensor cores, and it keeps full fp32
+// accuracy.  The kernel is bound by instruction issue.  A CTA owns 32 (16)
+// columns of one (sequence, head)'s state in registers; 4 (8) row groups of
+// 128 threads split the rows.  Two rows share one packed fp32 instruction.
+// Tokens come 16 at a time through shared memory, the next 16 already on
+// their way in registers; the row groups' shares of the outputs are summed
+// once per 16 tokens, so no barrier stands between tokens.
+#include "la_common.cuh"
+
+namespace ckda {
+namespace la {
+
+constexpr int kTile = 16;     // tokens per shared-memory tile
+constexpr int kRecThreads = 128;
+constexpr int kChunk = 64;    // tokens per chunk of the decay gradient
+static_assert(kChunk % kTile == 0, "tiles per chunk");
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+
+struct RecArgs {
+  const void *q, *k, *v;
+  Decay al;
+  // element (i, j) of a state of (n, h): base + (n H + h) DK DV + i si + j sj
+  const float* X0;  // or NULL
+  float* Xf;        // or NULL
+  int si, sj;
+  void* out;
+  // the state at each chunk's near bound (forward: its start, backward: its
+  // end), [slot, h, DK, DV], or NULL
+  float* kept;
+  const int32_t* cu;
+  int n_seqs, T, H, DV;
+  int* status;
+};
+
+template <int DK, int COLS, typename Tin, typename Tout, bool REV>
+__global__ void __launch_bounds__(kRecThreads) la_rec_kernel(const RecArgs p) {
+  constexpr int RG = kRecThreads / COLS;  // row groups
+  constexpr int RPT = DK / RG;            // rows per thread
+  constexpr int LQ = kTile * DK / kRecThreads;
+  constexpr int LV = kTile * COLS / kRecThreads;
+  static_assert(RPT % 2 == 0 && LQ >= 1 && LV >= 1, "shape");
+  __shared__ __align__(16) float sq[kTile][DK], sk[kTile][DK];
+  __shared__ float sv[kTile][COLS], sa[kTile], red[kTile][RG][COLS];
+
+  const int tid = threadIdx.x;
+  const int col = tid % COLS, g = tid / COLS;
+  // block index: column slice, then head, then sequence (longest first)
+  const int slices = p.DV / COLS;
+  const int j0 = (int)(blockIdx.x % slices) * COLS;
+  const int h = (int)(blockIdx.x / slices % p.H);
+  const int n = seq_longest_first(p.cu, p.n_seqs, (int)(blockIdx.x / slices / p.H));
+  const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
+  if (!sr.ok) return;
+  const int len = (int)(sr.end - sr.begin);
+  const int ntiles = (len + kTile - 1) / kTile;
+  const Tin* q = static_cast<const Tin*>(p.q);
+  const Tin* k = static_cast<const Tin*>(p.k);
+  const Tin* v = static_cast<const Tin*>(p.v);
+
+  const size_t st0 = ((size_t)n * p.H + h) * DK * p.DV;
+  const int i0 = g * RPT;
+  float2 X[RPT / 2];
+#pragma unroll
+  for (int r = 0; r < RPT / 2; ++r) {
+    X[r] = make_float2(0.f, 0.f);
+    if (p.X0 != nullptr) {
+      const float* b = p.X0 + st0 + (size_t)(j0 + col) * p.sj;
+      X[r] = make_float2(b[(size_t)(i0 + 2 * r) * p.si], b[(size_t)(i0 + 2 * r + 1) * p.si]);
+    }
+  }
+
+  float rq[LQ], rk[LQ], rv[LV], ra = 0.f;
+  // the tile's rows past the sequence's end are zero, so that what lies
+  // behind it is never read
+  auto fetch = [&](int tl) {
+    const int64_t t0 = sr.begin + (int64_t)tl * kTile;
+    const int rows = min(kTile, len - tl * kTile);
+#pragma unroll
+    for (int e = 0; e < LQ; ++e) {
+      const int x = tid + e * kRecThreads, t = x / DK, i = x % DK;
+      const size_t at = ((size_t)(t0 + t) * p.H + h) * DK + i;
+      rq[e] = t < rows ? Elem<Tin>::to_f32(q[at]) : 0.f;
+      rk[e] = t < rows ? Elem<Tin>::to_f32(k[at]) : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < LV; ++e) {
+      const int x = tid + e * kRecThreads, t = x / COLS, j = x % COLS;
+      rv[e] = t < rows ? Elem<Tin>::to_f32(v[((size_t)(t0 + t) * p.H + h) * p.DV + j0 + j]) : 0.f;
+    }
+    if (tid < kTile) ra = tid < rows ? p.al.at(t0 + tid, h) : 1.f;
+  };
+
+  const int64_t slot0 = p.kept != nullptr ? slot_of(p.cu, n, p.T, kChunk) : 0;
+  if (ntiles > 0) fetch(REV ? ntiles - 1 : 0);
+  for (int it = 0; it < ntiles; ++it) {
+    const int tl = REV ? ntiles - 1 - it : it;
+    const int64_t t0 = sr.begin + (int64_t)tl * kTile;
+    const int rows = min(kTile, len - tl * kTile);
+    __syncthreads();  // the last tile's reads are done
+#pragma unroll
+    for (int e = 0; e < LQ; ++e) {
+      const int x = tid + e * kRecThreads;
+      sq[x / DK][x % DK] = rq[e];
+      sk[x / DK][x % DK] = rk[e];
+    }
+#pragma unroll
+    for (int e = 0; e < LV; ++e) {
+      const int x = tid + e * kRecThreads;
+      sv[x / COLS][x % COLS] = rv[e];
+    }
+    if (tid < kTile) sa[tid] = ra;
+    __syncthreads();
+    if (it + 1 < ntiles) fetch(REV ? tl - 1 : tl + 1);
+
+    constexpr int per = kChunk / kTile;
+    if (p.kept != nullptr && (REV ? (tl % per == per - 1 || tl == ntiles - 1) : tl % per == 0)) {
+      float* o = p.kept + ((size_t)(slot0 + tl / per) * p.H + h) * DK * p.DV + j0 + col;
+#pragma unroll
+      for (int r = 0; r < RPT / 2; ++r) {
+        o[(size_t)(i0 + 2 * r) * p.DV] = X[r].x;
+        o[(size_t)(i0 + 2 * r + 1) * p.DV] = X[r].y;
+      }
+    }
+    // Backward in time the decay of token t acts behind its own term: it is
+    // applied with token t - 1's, and the tile's first token's at the end.
+#pragma unroll 2
+    for (int tt = 0; tt < rows; ++tt) {
+      const int t = REV ? rows - 1 - tt : tt;
+      const float a = REV ? (tt == 0 ? 1.f : sa[t + 1]) : sa[t];
+      const float vv = sv[t][col];
+      const float2 a2 = make_float2(a, a), v2 = make_float2(vv, vv);
+      float2 o = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < RPT / 2; ++r) {
+        const float2 k2 = *reinterpret_cast<const float2*>(&sk[t][i0 + 2 * r]);
+        const float2 q2 = *reinterpret_cast<const float2*>(&sq[t][i0 + 2 * r]);
+        X[r] = fma2(X[r], a2, mul2(k2, v2));
+        o = fma2(q2, X[r], o);
+      }
+      red[t][g][col] = o.x + o.y;
+    }
+    if (REV) {
+      const float2 a2 = make_float2(sa[0], sa[0]);
+#pragma unroll
+      for (int r = 0; r < RPT / 2; ++r) X[r] = mul2(X[r], a2);
+    }
+    __syncthreads();
+    if (p.out != nullptr) {
+      Tout* out = static_cast<Tout*>(p.out);
+#pragma unroll
+      for (int e = 0; e < LV; ++e) {
+        const int x = tid + e * kRecThreads, t = x / COLS, j = x % COLS;
+        if (t < rows) {
+          float s = red[t][0][j];
+#pragma unroll
+          for (int gg = 1; gg < RG; ++gg) s += red[t][gg][j];
+          out[((size_t)(t0 + t) * p.H + h) * p.DV + j0 + j] = Elem<Tout>::from_f32(s);
+        }
+      }
+    }
+  }
+  if (p.Xf != nullptr) {
+    float* b = p.Xf + st0 + (size_t)(j0 + col) * p.sj;
+#pragma unroll
+    for (int r = 0; r < RPT / 2; ++r) {
+      b[(size_t)(i0 + 2 * r) * p.si] = X[r].x;
+      b[(size_t)(i0 + 2 * r + 1) * p.si] = X[r].y;
+    }
+  }
+}
+
+template <int DK, int COLS, typename Tin, typename Tout>
+static cudaError_t rec_launch(const RecArgs& a, bool rev, cudaStream_t st) {
+  const unsigned grid = (unsigned)(a.DV / COLS) * a.H * a.n_seqs;
+  if (rev)
+    la_rec_kernel<DK, COLS, Tin, Tout, true><<<grid, kRecThreads, 0, st>>>(a);
+  else
+    la_rec_kernel<DK, COLS, Tin, Tout, false><<<grid, kRecThreads, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+template <int DK, typename Tin, typename Tout>
+static cudaError_t rec_cols(const RecArgs& a, bool rev, cudaStream_t st) {
+  return a.DV == 16 ? rec_launch<DK, 16, Tin, Tout>(a, rev, st)
+                    : rec_launch<DK, 32, Tin, Tout>(a, rev, st);
+}
+
+template <typename Tin, typename Tout>
+static cudaError_t rec_rows(int dk, const RecArgs& a, bool rev, cudaStream_t st) {
+  switch (dk) {
+    case 16: return rec_cols<16, Tin, Tout>(a, rev, st);
+    case 32: return rec_cols<32, Tin, Tout>(a, rev, st);
+    case 64: return rec_cols<64, Tin, Tout>(a, rev, st);
+    case 128: return rec_cols<128, Tin, Tout>(a, rev, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+static cudaError_t rec(int dtype, int out_dtype, int dk, const RecArgs& a, bool rev,
+                       cudaStream_t st) {
+  if (dtype == CKDA_BF16)
+    return out_dtype == CKDA_BF16 ? rec_rows<__nv_bfloat16, __nv_bfloat16>(dk, a, rev, st)
+                                  : rec_rows<__nv_bfloat16, float>(dk, a, rev, st);
+  return out_dtype == CKDA_BF16 ? rec_rows<float, __nv_bfloat16>(dk, a, rev, st)
+                                : rec_rows<float, float>(dk, a, rev, st);
+}
+
+// ---- the decay's gradient --------------------------------------------------------
+//
+// Within a chunk (positions 0..L-1, start state S, adjoint G of the state at
+// its end, D(i, j) = a_{j+1} .. a_i):
+//   da_t = sum_{i >= t > j} D(i, t) D(t-1, j) (q_i.k_j) (do_i.v_j)
+//        + head_t sum_{i >= t} D(i, t) x_i + tail_t sum_{j < t} D(t-1, j) y_j
+//        + head_t tail_t <S, G>
+// with x_i = do_i . S^T q_i, y_j = v_j . G^T k_j, head_t = a_0 .. a_{t-1} and
+// tail_t = a_{t+1} .. a_{L-1}: the products leave a_t out instead of dividing
+// by it, so a zero decay has its gradient too.  The double sum is
+//   U_t[j] = W[t][j] + a_{t+1} U_{t+1}[j],   sum_j D(t-1, j) U_t[j],
+// one column j per thread.
+struct DalphaArgs {
+  const void *q, *k, *v, *dO;
+  Decay al;
+  const float* St;  // S^T at the chunks' starts [slot, h, DV, DK]
+  const float* G;   // G at the chunks' ends [slot, h, DK, DV]
+  float* da;        // [tokens, H]
+  const int32_t* cu;
+  int n_seqs, T, H, DK, DV;
+  int* status;
+};
+
+constexpr int kDaThreads = 256;
+constexpr int kSlab = 16;  // inner dimension per shared-memory slab (head sizes are multiples)
+
+template <typename Tin>
+__global__ void __launch_bounds__(kDaThreads) la_dalpha_kernel(const DalphaArgs p) {
+  constexpr int C = kChunk;
+  __shared__ float sa[C], sx[C], sy[C], head[C], tail[C], zs[kDaThreads / 32];
+  __shared__ float A[kSlab][C + 4], B[kSlab][C + 4];
+  __shared__ float W[C][C + 1], E[C][C + 1];
+  const int tid = threadIdx.x;
+  const int h = blockIdx.y;
+  int n, c;
+  if (!slot_chunk(p.cu, p.n_seqs, p.T, C, blockIdx.x, &n, &c)) return;
+  const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
+  if (!sr.ok) return;
+  const int64_t t0 = sr.begin + (int64_t)c * C;
+  const int L = (int)min((int64_t)C, sr.end - t0);
+  const Tin* q = static_cast<const Tin*>(p.q);
+  const Tin* k = static_cast<const Tin*>(p.k);
+  const Tin* v = static_cast<const Tin*>(p.v);
+  const Tin* dO = static_cast<const Tin*>(p.dO);
+  const int ty = tid / 16, tx = tid % 16;  // this thread's 4 x 4 block of a C x C product
+
+  if (tid < C) {
+    sa[tid] = tid < L ? p.al.at(t0 + tid, h) : 1.f;
+    sx[tid] = 0.f;
+    sy[tid] = 0.f;
+  }
+  // acc[a][b] += sum_d Arow[ty * 4 + a][d] * Brow[tx * 4 + b][d]
+  auto rows = [&](const Tin* x, int D, int d0, float (*dst)[C + 4]) {
+    for (int e = tid; e < C * kSlab; e += kDaThreads) {
+      const int r = e / kSlab, d = e % kSlab;
+      dst[d][r] = r < L ? Elem<Tin>::to_f32(x[((size_t)(t0 + r) * p.H + h) * D + d0 + d]) : 0.f;
+    }
+  };
+  auto mac = [&](float (*acc)[4]) {
+#pragma unroll
+    for (int d = 0; d < kSlab; ++d) {
+      float a[4], b[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = A[d][ty * 4 + e];
+        b[e] = B[d][tx * 4 + e];
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+    }
+  };
+  float s1[4][4] = {}, s2[4][4] = {};
+  for (int d0 = 0; d0 < p.DK; d0 += kSlab) {
+    __syncthreads();
+    rows(q, p.DK, d0, A);
+    rows(k, p.DK, d0, B);
+    __syncthreads();
+    mac(s1);
+  }
+  for (int d0 = 0; d0 < p.DV; d0 += kSlab) {
+    __syncthreads();
+    rows(dO, p.DV, d0, A);
+    rows(v, p.DV, d0, B);
+    __syncthreads();
+    mac(s2);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) W[ty * 4 + i][tx * 4 + j] = s1[i][j] * s2[i][j];
+
+  // x and y: rows of [q S] . do and [k G] . v, C columns of the product at a time
+  const size_t st = ((size_t)blockIdx.x * p.H + h) * p.DK * p.DV;
+  for (int which = 0; which < 2; ++which) {
+    const float* M = (which ? p.G : p.St) + st;
+    for (int j0 = 0; j0 < p.DV; j0 += C) {
+      float s[4][4] = {};
+      for (int d0 = 0; d0 < p.DK; d0 += kSlab) {
+        __syncthreads();
+        rows(which ? k : q, p.DK, d0, A);
+        for (int e = tid; e < C * kSlab; e += kDaThreads) {
+          // S^T rows run over d_k, G rows over d_v: read along the rows
+          const int j = which ? e % C : e / kSlab, d = which ? e / C : e % kSlab;
+          float x = 0.f;
+          if (j0 + j < p.DV)
+            x = which ? M[(size_t)(d0 + d) * p.DV + j0 + j] : M[(size_t)(j0 + j) * p.DK + d0 + d];
+          B[d][j] = x;
+        }
+        __syncthreads();
+        mac(s);
+      }
+      const Tin* y = which ? v : dO;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = ty * 4 + i;
+        float part = 0.f;
+        if (r < L) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int jj = j0 + tx * 4 + j;
+            if (jj < p.DV)
+              part = fmaf(s[i][j], Elem<Tin>::to_f32(y[((size_t)(t0 + r) * p.H + h) * p.DV + jj]),
+                          part);
+          }
+        }
+#pragma unroll
+        for (int o = 8; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        if (tx == 0) (which ? sy : sx)[r] += part;  // one writer per row
+      }
+    }
+  }
+  // <S, G>: both read along d_k of S^T
+  float z = 0.f;
+  for (int e = tid; e < p.DK * p.DV; e += kDaThreads) {
+    const int i = e % p.DK, j = e / p.DK;
+    z = fmaf(p.St[st + e], p.G[st + (size_t)i * p.DV + j], z);
+  }
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+  if (tid % 32 == 0) zs[tid / 32] = z;
+  __syncthreads();
+
+  if (tid < C) {
+    // E[t][j] = D(t - 1, j), then times U_t[j]
+    const int j = tid;
+    float d = 1.f;
+    for (int t = j + 1; t < L; ++t) {
+      E[t][j] = d;
+      d *= sa[t];
+    }
+    float u = 0.f;
+    for (int t = L - 1; t > j; --t) {
+      u = fmaf(t + 1 < L ? sa[t + 1] : 0.f, u, W[t][j]);
+      E[t][j] *= u;
+    }
+  } else if (tid == C) {
+    float d = 1.f;
+    for (int t = 0; t < L; ++t) {
+      head[t] = d;
+      d *= sa[t];
+    }
+    float x = 0.f;
+    for (int t = L - 1; t >= 0; --t) {
+      x = fmaf(t + 1 < L ? sa[t + 1] : 0.f, x, sx[t]);
+      sx[t] = x;
+    }
+  } else if (tid == C + 32) {
+    float d = 1.f;
+    for (int t = L - 1; t >= 0; --t) {
+      tail[t] = d;
+      d *= sa[t];
+    }
+    float y = 0.f;
+    for (int t = 0; t < L; ++t) {
+      const float own = sy[t];
+      sy[t] = y;
+      y = fmaf(sa[t], y, own);
+    }
+  }
+  __syncthreads();
+  if (tid < L) {
+    const int t = tid;
+    float zz = 0.f;
+#pragma unroll
+    for (int w = 0; w < kDaThreads / 32; ++w) zz += zs[w];
+    float s = 0.f;
+    for (int j = 0; j < t; ++j) s += E[t][j];
+    s = fmaf(head[t], sx[t], s);
+    s = fmaf(tail[t], sy[t], s);
+    s = fmaf(head[t] * tail[t], zz, s);
+    p.da[(size_t)(t0 + t) * p.H + h] = s;
+  }
+}
+
+// da[h] = the sum over the tokens of per-token gradients [tokens, H]: one CTA
+// per head, a fixed order, sums in 64 bits.
+__global__ void __launch_bounds__(256) la_dalpha_sum_kernel(const float* __restrict__ part,
+                                                            float* __restrict__ da, int64_t tokens,
+                                                            int H) {
+  __shared__ double red[256];
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (int64_t t = threadIdx.x; t < tokens; t += 256) s += (double)part[t * H + h];
+  red[threadIdx.x] = s;
+  __syncthreads();
+#pragma unroll
+  for (int w = 128; w >= 1; w >>= 1) {
+    if (threadIdx.x < w) red[threadIdx.x] += red[threadIdx.x + w];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) da[h] = (float)red[0];
+}
+
+}  // namespace la
+
+cudaError_t launch_la_fwd_simt(int dtype, int out_dtype, int dk, int dv, const void* q,
+                               const void* k, const void* v, const float* alpha, int per_head,
+                               const float* S0, const int32_t* cu, void* out, float* S_final,
+                               int n_seqs, int T, int H, int* status, cudaStream_t stream) {
+  const la::RecArgs a{q,   k,       v,  {alpha, H, per_head}, S0, S_final, dv, 1,
+                      out, nullptr, cu, n_seqs, T, H, dv, status};
+  return la::rec(dtype, out_dtype, dk, a, false, stream);
+}
+
+cudaError_t launch_la_dalpha_sum(const float* part, float* da, int64_t tokens, int H,
+                                 cudaStream_t stream) {
+  la::la_dalpha_sum_kernel<<<H, 256, 0, stream>>>(part, da, tokens, H);
+  return cudaGetLastError();
+}
+
+// S^T and G at the chunks' bounds, then (decay per head) its gradient per token.
+size_t la_bwd_simt_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen,
+                                   bool per_head) {
+  const size_t slots = (size_t)la::chunk_slots(varlen, n_seqs, T, la::kChunk);
+  const size_t tokens = varlen ? (size_t)T : (size_t)n_seqs * T;
+  return 2 * slots * H * dk * dv * 4 + (per_head ? (tokens * H * 4 + 255) / 256 * 256 : 0);
+}
+
+cudaError_t launch_la_bwd_simt(int dtype, int dk_, int dv_, const void* q, const void* k,
+                               const void* v, const float* alpha, int per_head, const float* S0,
+                               const int32_t* cu, const void* dO, const float* dSf, void* dq,
+                               void* dk, void* dv, float* dalpha, float* dS0, void* ws, int n_seqs,
+                               int T, int H, int* status, cudaStream_t stream) {
+  const bool varlen = cu != nullptr;
+  const size_t slots = (size_t)la::chunk_slots(varlen, n_seqs, T, la::kChunk);
+  const int64_t tokens = varlen ? (int64_t)T : (int64_t)n_seqs * T;
+  float* St = static_cast<float*>(ws);
+  float* G = St + slots * H * dk_ * dv_;
+  float* part = per_head ? G + slots * H * dk_ * dv_ : dalpha;
+  const la::Decay al{alpha, H, per_head};
+  // (state, stride of its first index, stride of its second): S^T, G, G^T
+  const la::RecArgs aq{dO, v, k, al, S0, nullptr, 1, dv_, dq, St, cu, n_seqs, T, H, dk_, status};
+  const la::RecArgs av{k, q, dO, al, dSf, dS0, dv_, 1, dv, G, cu, n_seqs, T, H, dv_, status};
+  const la::RecArgs ak{v, dO, q, al, dSf, nullptr, 1, dv_, dk, nullptr, cu, n_seqs, T, H, dk_,
+                       status};
+  cudaError_t e = la::rec(dtype, dtype, dv_, aq, false, stream);
+  if (e == cudaSuccess) e = la::rec(dtype, dtype, dk_, av, true, stream);
+  if (e == cudaSuccess) e = la::rec(dtype, dtype, dv_, ak, true, stream);
+  if (e != cudaSuccess) return e;
+  if (slots > 0) {
+    const la::DalphaArgs d{q, k, v, dO, al, St, G, part, cu, n_seqs, T, H, dk_, dv_, status};
+    const dim3 grid((unsigned)slots, H);
+    if (dtype == CKDA_BF16)
+      la::la_dalpha_kernel<__nv_bfloat16><<<grid, la::kDaThreads, 0, stream>>>(d);
+    else
+      la::la_dalpha_kernel<float><<<grid, la::kDaThreads, 0, stream>>>(d);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return per_head ? launch_la_dalpha_sum(part, dalpha, tokens, H, stream) : cudaSuccess;
+}
+
+}  // namespace ckda

@@ -464,6 +464,120 @@ CKDA_API int ckda_sfda_decode_step(const void* q, const void* k, const void* v,
                                    float* S_inout, void* out, int B, int H, int d_k, int d_v,
                                    int dtype, int out_dtype, void* stream);
 
+/*
+ * Head-decay linear attention: the recurrence without the delta rule, one
+ * decay per head and token, or one per head:
+ *
+ *     S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   a_t in [-1, 1].
+ *
+ * ("Understanding Kimi Delta Attention and its Extensions": the gated linear
+ * recurrence that the delta rule extends; it is the Gated DeltaNet-2 form
+ * with the erase gate 0, the write gate 1 and a scalar decay.)  Products of
+ * decays are running products, never quotients or logarithms: zero and
+ * negative decays are exact.  Rules as for ckda_fwd_chunked, and:
+ *
+ *   alpha           [B, T, H] ([T, H] packed) fp32, or [H] when
+ *                   alpha_per_head is 1.
+ *   d_k, d_v        each in {16, 32, 64, 128}; H at most 65535 and
+ *                   B * H * 8 below 2^31, else CKDA_ERR_UNSUPPORTED.
+ *   out             overlaps no other tensor; S_final may equal S0 and
+ *                   otherwise overlaps none.  An overlap returns
+ *                   CKDA_ERR_INVALID_ARG.
+ *   workspace       at least ckda_la_fwd_workspace_bytes() bytes, 256-byte
+ *                   aligned, overlapping no tensor; calls that may run at
+ *                   the same time need workspaces of their own.  The query
+ *                   may return 0, workspace may then be NULL.
+ * Tokens behind cu_seqlens' last offset are neither read nor written.  With
+ * bf16 inputs and d_k, d_v large enough for the tensor cores the products'
+ * operands are bf16, their sums fp32, and a row of out is within a few bf16
+ * roundings of the exact one; S_final keeps fp32 accuracy.
+ */
+CKDA_API int ckda_la_fwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
+                                 const float* S0, const int32_t* cu_seqlens, void* out,
+                                 float* S_final, int B, int T, int H, int d_k, int d_v,
+                                 int alpha_per_head, int dtype, int out_dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+CKDA_API int64_t ckda_la_fwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int dtype,
+                                             int varlen);
+
+/*
+ * ckda_la_bwd_chunked -- the gradients of a scalar loss with respect to q, k,
+ * v, alpha and S0, given dO = dL/dout (dtype, shaped like v) and dS_final =
+ * dL/dS_final (fp32 [B, H, d_k, d_v], or NULL = 0).  dq, dk, dv are shaped
+ * and typed like q, k, v; dalpha (fp32) is shaped like alpha, summed over the
+ * tokens when alpha_per_head is 1; dS0 (fp32) may be NULL.  The gradient of a
+ * zero decay is that of the recurrence (no division by a_t).  No output may
+ * overlap another tensor.  Every output element is written by every call
+ * (tokens behind the last sequence excepted), sums are in a fixed order.
+ */
+CKDA_API int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
+                                 const float* S0, const int32_t* cu_seqlens, const void* dO,
+                                 const float* dS_final, void* dq, void* dk, void* dv,
+                                 float* dalpha, float* dS0, int B, int T, int H, int d_k, int d_v,
+                                 int alpha_per_head, int dtype, void* workspace,
+                                 size_t workspace_bytes, void* stream);
+CKDA_API int64_t ckda_la_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v,
+                                             int alpha_per_head, int dtype, int varlen);
+
+/*
+ * ckda_la_decode_step -- one token for every (sequence, head), in place on
+ * the state: S <- a S + k v^T, o = S^T q in fp32.  q, k [B, H, d_k], v, out
+ * [B, H, d_v], alpha [B, H] or [H], S_inout [B, H, d_k, d_v] fp32; S_inout and
+ * out overlap no other tensor.
+ */
+CKDA_API int ckda_la_decode_step(const void* q, const void* k, const void* v, const float* alpha,
+                                 float* S_inout, void* out, int B, int H, int d_k, int d_v,
+                                 int alpha_per_head, int dtype, int out_dtype, void* stream);
+
+/* The norm's mean: c |x|^2 + eps with c = 1 (unit length) or 1 / d. */
+enum {
+  CKDA_NORM_L2 = 0,
+  CKDA_NORM_RMS = 1
+};
+
+/*
+ * ckda_qk_norm_rope -- norm of every head of the queries and the keys and
+ * their rotation by position, in one pass: what the recurrences above take as
+ * q and k.  Per row x of d channels
+ *     y = x (c |x|^2 + eps)^(-1/2) * w,   out = R(position) y,
+ * R turning channel pair p of the first `rot` channels by position *
+ * inv_freq[p] radians: pairs (p, p + rot / 2), or (2p, 2p + 1) when
+ * interleaved is 1.  Computed in fp32 (the angles are reduced in 64 bits, so
+ * far positions keep their accuracy), rounded once to out_dtype.
+ *
+ *   q, k         rows [Hq, d] and [Hk, d] of token t at q + t * q_stride and
+ *                k + t * k_stride (elements, multiples of 16 bytes): both may
+ *                lie in one projection's output.  Hq or Hk may be 0.
+ *   wq, wk       [d] fp32 or NULL (ones).
+ *   positions    [tokens] int32, inv_freq [rot / 2] fp32; unused when rot = 0.
+ *   q_out, k_out [tokens, Hq, d], [tokens, Hk, d] (out_dtype), contiguous;
+ *                may be q and k themselves when those are contiguous and of
+ *                the same type, and overlap nothing otherwise.
+ *   d in {16, 32, 64, 128}; rot a multiple of 8, 0 <= rot <= d; eps >= 0 (a
+ *   row of zeros with eps = 0 gives zeros).
+ */
+CKDA_API int ckda_qk_norm_rope(const void* q, const void* k, const float* wq, const float* wk,
+                               const int32_t* positions, const float* inv_freq, void* q_out,
+                               void* k_out, int64_t tokens, int Hq, int Hk, int d, int rot,
+                               int interleaved, int norm, float eps, int64_t q_stride,
+                               int64_t k_stride, int dtype, int out_dtype, void* stream);
+
+/*
+ * ckda_qk_norm_rope_bwd -- its gradients: dq, dk (contiguous, dtype) and, each
+ * unless NULL, dwq, dwk ([d] fp32, summed over tokens and heads in a fixed
+ * order), given dq_out, dk_out (contiguous, dtype).  The workspace
+ * (ckda_qk_norm_rope_bwd_workspace_bytes(), 256-byte aligned) is needed when
+ * dwq or dwk is.  No output may overlap another tensor.
+ */
+CKDA_API int ckda_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const float* wk,
+                                   const int32_t* positions, const float* inv_freq,
+                                   const void* dq_out, const void* dk_out, void* dq, void* dk,
+                                   float* dwq, float* dwk, int64_t tokens, int Hq, int Hk, int d,
+                                   int rot, int interleaved, int norm, float eps, int64_t q_stride,
+                                   int64_t k_stride, int dtype, void* workspace,
+                                   size_t workspace_bytes, void* stream);
+CKDA_API int64_t ckda_qk_norm_rope_bwd_workspace_bytes(int d);
+
 /* Human-readable text for a CKDA_* status code (static storage). */
 CKDA_API const char* ckda_status_string(int status);
 
