@@ -1,0 +1,633 @@
+// Head-decay linear attention on the tensor cores (tcgen05): bf16 inputs,
+// d_k = 128, d_v a multiple of 64 (sm_100a).
+//
+// Per chunk of C = 128 tokens (start state S, D(i, j) = a_{j+1} .. a_i):
+//   O = (D o Q K^T) V + diag(pre) Q S,   S' = gamma S + K^T diag(suf) V,
+// pre_i = a_0 .. a_i, suf_j = a_{j+1} .. a_{C-1}, gamma = a_0 .. a_{C-1}: two
+// products on either side of the scores, and the state touched once per
+// chunk.  The work is one read of q, k, v and one write of out: bound by HBM
+// bandwidth, if the products and what feeds them keep up.
+//
+// One CTA walks the chunks of a (sequence, head) for 64 of the d_v columns
+// (the slices of a head read the same q and k at about the same time, from L2
+// but once).  Its warps have fixed roles and pass each chunk on through
+// mbarriers:
+//   warps 0..3   scores: tensor memory -> times the decays, masked -> bf16
+//                operand back in tensor memory (thread = row i)
+//   warps 4..7   state: V's rows times suf as bf16 operands in shared memory;
+//                S' = gamma S + product, in fp32 registers (thread = row of
+//                d_k), its bf16 copy for the next chunk
+//   warps 8..11  out: pre_i (Q S) + (P V), rounded and stored
+//   warp 12      every MMA (one thread)
+//   warp 13      every TMA load (one thread): q, k, v two chunks deep
+//   warp 14      the decays' products of each chunk
+//
+// Decays are running products within aligned blocks of 32 tokens: prefW_i
+// from the block's start through i, sufW_j from j + 1 to the block's end,
+// tot_b of whole blocks; D(i, j) across blocks is prefW_i tot .. tot sufW_j.
+// No logarithm and no division: zero and negative decays are exact, and
+// underflow goes to zero.
+//
+// Roundings: the scores (after their decays) and the state's copy that the
+// queries read are rounded once to bf16, like the inputs; both only reach
+// out.  The state itself stays at fp32 accuracy: diag(suf) V is split into
+// three bf16 terms (24 bits), whose products with the exact bf16 K are one
+// MMA with the three terms side by side (N = 192).  Side by side they also
+// read K from shared memory once instead of three times; with N = 64 the
+// product would be bound by that read.
+//
+// A sequence may be split into segments that run at the same time (few
+// sequences and heads): a first launch computes each segment's own end state
+// (K, V only), the second starts every segment from their decayed sum.
+
+#include "la_common.cuh"
+#include "sm100.cuh"
+#include "la_tc.cuh"
+
+namespace ckda {
+namespace la {
+
+using namespace sm100;
+
+namespace fw {
+
+constexpr int C = 128;
+constexpr int DK = 128;
+constexpr int BV = 64;  // d_v columns per CTA
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
+
+// shared memory
+constexpr uint32_t OFF_Q = 0;                    // 2 stages [128][128] bf16, two 64-column atoms
+constexpr uint32_t OFF_K = 65536;                // 2 stages, the same
+constexpr uint32_t OFF_V = 131072;               // 2 stages [128][64]
+constexpr uint32_t OFF_VW = 163840;              // diag(suf) V: 3 terms [128][64]
+constexpr uint32_t OFF_SB = OFF_VW + 3 * 16384;  // bf16 state [128][64]
+constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x {prefW[128], sufW[128], tot[4]} fp32
+constexpr uint32_t kDecBytes = 1024 + 16;
+constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
+constexpr uint32_t OFF_MISC = OFF_BAR + 176;     // tensor-memory base, the sequence
+constexpr uint32_t kSmem = OFF_MISC + 16;
+static_assert(kSmem <= 232448, "shared memory");
+
+// mbarriers, byte offsets from OFF_BAR; each completes once per chunk (those
+// with two stages once per two)
+constexpr uint32_t B_Q = 0, B_K = 16, B_V = 32;  // stage loaded, + 8 (c & 1)
+constexpr uint32_t B_SC = 48;    // Q K^T complete (tensor core); then P's buffer is free too
+constexpr uint32_t B_P = 56;     // scores read, P written
+constexpr uint32_t B_VW = 64;    // diag(suf) V written, V's and K's tail rows cleared
+constexpr uint32_t B_SB = 72;    // the state's operand written, the product read
+constexpr uint32_t B_OE = 80;    // Q S and P V read
+// complete (tensor core), + 8 (c & 1): the copy thread, which nothing holds
+// to the chunk, waits for these too
+constexpr uint32_t B_D = 88;     // K^T diag(suf) V
+constexpr uint32_t B_QS = 104;   // Q S
+constexpr uint32_t B_O = 120;    // Q S and P V
+constexpr uint32_t B_DEC = 136;  // decays of a chunk written, + 8 (c & 1)
+constexpr uint32_t B_DECE = 152; // and read, + 8 (c & 1)
+
+// tensor-memory columns
+constexpr uint32_t TM_SC = 0;    // Q K^T
+constexpr uint32_t TM_P = 128;   // P, bf16 pairs
+constexpr uint32_t TM_O1 = 192;  // Q S
+constexpr uint32_t TM_O2 = 256;  // P V
+constexpr uint32_t TM_D = 320;   // K^T diag(suf) V, three terms
+constexpr uint32_t kTmemCols = 512;
+
+constexpr int kThreads = 480;
+
+struct Args {
+  Decay al;
+  const float* S0;
+  const int32_t* cu;
+  void* out;
+  float* Sf;
+  int n_seqs, T, H, DV;
+  int* status;
+  // segments per sequence; part[(n H + h) seg_n + g]: for g > 0 the end state
+  // of segment g - 1 (segment 0's from S0, the others' from zero), for g = 0
+  // a copy of S0; dec: the segments' decays
+  int seg_n;
+  float* part;
+  float* dec;
+};
+
+// SUM: the segments' own end states only (segments 0 .. seg_n - 2)
+template <typename Tout, bool SUM>
+__global__ void __launch_bounds__(kThreads, 1)
+la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v, const Args p) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // (the swizzled tiles need this; the base of dynamic shared memory has it)
+  if ((sb & 1023u) != 0) {
+    set_status(p.status, CKDA_ERR_CUDA);
+    return;
+  }
+
+  const int slices = p.DV / BV;
+  const int nseg = SUM ? p.seg_n - 1 : p.seg_n;
+  // block index: column slice, then segment, then head, then sequence (longest first)
+  int b = blockIdx.x;
+  const int j0 = (b % slices) * BV;
+  b /= slices;
+  const int seg = b % nseg;
+  b /= nseg;
+  const int h = b % p.H;
+  int* pick = reinterpret_cast<int*>(sm + OFF_MISC + 4);
+  const int n = longest_first(p.cu, p.n_seqs, b / p.H, pick);
+  const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
+  if (!sr.ok) return;
+
+  const uint32_t bar = sb + OFF_BAR;
+  if (tid == 0) {
+    for (int i = 0; i < 6; ++i) mbar_init(bar + 8 * i, 1);
+    mbar_init(bar + B_SC, 1);
+    mbar_init(bar + B_P, 128);
+    mbar_init(bar + B_VW, 128);
+    mbar_init(bar + B_SB, 128);
+    mbar_init(bar + B_OE, 128);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + B_D + 8 * i, 1);
+      mbar_init(bar + B_QS + 8 * i, 1);
+      mbar_init(bar + B_O + 8 * i, 1);
+      mbar_init(bar + B_DEC + 8 * i, 32);
+      mbar_init(bar + B_DECE + 8 * i, SUM ? 128 : 384);
+    }
+    fence_mbar_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  if (warp == 0) {
+    tmem_alloc(sb + OFF_MISC, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC);
+
+  const int nck_all = (int)((sr.end - sr.begin + C - 1) / C);
+  const int cbeg = (int)((int64_t)seg * nck_all / p.seg_n);
+  const int nck = (int)((int64_t)(seg + 1) * nck_all / p.seg_n) - cbeg;
+  const int64_t tok0 = sr.begin + (int64_t)cbeg * C;
+  auto len_of = [&](int c) -> int {
+    const int64_t left = sr.end - (tok0 + (int64_t)c * C);
+    return left < C ? (int)left : C;
+  };
+  auto wait = [&](uint32_t off, uint32_t par) -> bool {
+    return mbar_wait_bounded(bar + off, par & 1u, kWaitNs);
+  };
+  const float* dec0 = reinterpret_cast<const float*>(sm + OFF_DEC);
+  auto pref = [&](int c) { return dec0 + (c & 1) * (kDecBytes / 4); };
+  auto suff = [&](int c) { return pref(c) + 128; };
+  auto tots = [&](int c) { return pref(c) + 256; };
+  bool ok = true;
+  // the copy thread's loads, bit 2 (Q, K, V) + stage: issued, and the parity of the last one
+  uint32_t pend = 0, pend_par = 0;
+  bool mma_open = false;
+  uint32_t mma_off = 0, mma_par = 0;
+
+  if (warp < 4) {
+    // ---- scores ---------------------------------------------------------------------------
+    if constexpr (!SUM) {
+      const int i = tid;  // row
+      const uint32_t row = tmem + ((uint32_t)(32 * warp) << 16);
+      {
+        // blocks right of the diagonal stay zero
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = 0u;
+        for (int J = warp + 1; J < 4; ++J) tmem_st16(row + TM_P + 16 * J, z);
+        tmem_st_wait();
+      }
+      auto load_a = [&](int c) -> float {
+        return (c < nck && i < len_of(c)) ? p.al.at(tok0 + (int64_t)c * C + i, h) : 1.f;
+      };
+      float a = load_a(0);
+      for (int c = 0; c < nck; ++c) {
+        const float a_next = load_a(c + 1);
+        if (!(ok = wait(B_DEC + 8 * (c & 1), c >> 1))) break;
+        const float* sw = suff(c);
+        const float* tot = tots(c);
+        float d = pref(c)[i];  // times the blocks between, going left
+        if (!(ok = wait(B_SC, c))) break;
+        tc_fence_after();
+        float s[32];
+        uint32_t w[16];
+        // the diagonal block: D(i, j) runs down from 1 at j = i
+        tmem_ld32(row + TM_SC + 32 * warp, s);
+        tmem_ld_wait();
+        {
+          float run = 1.f;
+#pragma unroll
+          for (int j = 31; j >= 0; --j) {
+            const float aj = __shfl_sync(0xffffffffu, a, j);
+            s[j] = j <= lane ? s[j] * run : 0.f;
+            run = j <= lane ? run * aj : run;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+        tmem_st16(row + TM_P + 16 * warp, w);
+        for (int J = warp - 1; J >= 0; --J) {
+          tmem_ld32(row + TM_SC + 32 * J, s);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 x = *reinterpret_cast<const float4*>(sw + 32 * J + 4 * e);
+            w[2 * e] = pack_bf16x2(s[4 * e] * (d * x.x), s[4 * e + 1] * (d * x.y));
+            w[2 * e + 1] = pack_bf16x2(s[4 * e + 2] * (d * x.z), s[4 * e + 3] * (d * x.w));
+          }
+          tmem_st16(row + TM_P + 16 * J, w);
+          d *= tot[J];
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(bar + B_P);
+        mbar_arrive(bar + B_DECE + 8 * (c & 1));
+        a = a_next;
+      }
+    }
+  } else if (warp < 8) {
+    // ---- state ----------------------------------------------------------------------------
+    const int q4 = warp & 3;
+    const int r = tid - 128;  // token j of V, row i of the state
+    const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
+    float S[BV];
+#pragma unroll
+    for (int e = 0; e < BV; ++e) S[e] = 0.f;
+    const size_t unit = (size_t)n * p.H + h;
+    const size_t at = ((size_t)r * p.DV) + j0;  // this row's columns in a state
+    const size_t stsz = (size_t)DK * p.DV;
+    auto add = [&](const float* src, float f) {
+#pragma unroll
+      for (int e = 0; e < BV; e += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(src + e);
+        S[e] = fmaf(f, x.x, S[e]);
+        S[e + 1] = fmaf(f, x.y, S[e + 1]);
+        S[e + 2] = fmaf(f, x.z, S[e + 2]);
+        S[e + 3] = fmaf(f, x.w, S[e + 3]);
+      }
+    };
+    auto put = [&](float* dst) {
+#pragma unroll
+      for (int e = 0; e < BV; e += 4)
+        *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+    };
+    if (seg == 0) {
+      // (with segments the last one may write S_final over S0 before this
+      // block starts: the first launch keeps a copy)
+      const float* s0 = p.S0;
+      if (s0 != nullptr) {
+        if (!SUM && p.seg_n > 1)
+          add(p.part + unit * p.seg_n * stsz + at, 1.f);
+        else
+          add(s0 + unit * stsz + at, 1.f);
+      }
+      if (SUM && s0 != nullptr) put(p.part + unit * p.seg_n * stsz + at);
+    } else if (!SUM) {
+      float f = 1.f;
+      for (int g = seg; g >= 1; --g) {
+        add(p.part + (unit * p.seg_n + g) * stsz + at, f);
+        f *= p.dec[unit * p.seg_n + g - 1];
+      }
+    }
+    auto operand = [&]() {
+      if constexpr (!SUM) {
+#pragma unroll
+        for (int c8 = 0; c8 < BV / 8; ++c8) {
+          const float* x = S + 8 * c8;
+          *reinterpret_cast<uint4*>(sm + OFF_SB + sw128_chunk(r, 8 * c8, 128)) =
+              make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                         pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        }
+        fence_proxy_async_smem();
+      }
+    };
+    operand();
+    mbar_arrive(bar + B_SB);
+    float total = 1.f;
+    for (int c = 0; c < nck; ++c) {
+      const int st = c & 1;
+      const int len = len_of(c);
+      if (!(ok = wait(B_DEC + 8 * st, c >> 1))) break;
+      const float* tot = tots(c);
+      float wgt = suff(c)[r];
+      for (int bk = q4 + 1; bk < 4; ++bk) wgt *= tot[bk];
+      const float gamma = (tot[0] * tot[1]) * (tot[2] * tot[3]);
+      mbar_arrive(bar + B_DECE + 8 * st);
+      if (!(ok = wait(B_V + 8 * st, c >> 1) && (len == C || wait(B_K + 8 * st, c >> 1)))) break;
+      if (r < len) {
+#pragma unroll
+        for (int c8 = 0; c8 < BV / 8; ++c8) {
+          const uint32_t o = sw128_chunk(r, 8 * c8, 128);
+          const uint4 raw = *reinterpret_cast<const uint4*>(sm + OFF_V + st * 16384 + o);
+          const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+          uint32_t t1[4], t2[4], t3[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) split3(in[e], wgt, &t1[e], &t2[e], &t3[e]);
+          uint8_t* d = sm + OFF_VW + o;
+          *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(d + 16384) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+          *reinterpret_cast<uint4*>(d + 32768) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+        }
+      } else {
+        // past the sequence's end lie other tokens, or none: V and K rows
+        // cleared, so that no product meets what is not finite there
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c8 = 0; c8 < BV / 8; ++c8) {
+          const uint32_t o = sw128_chunk(r, 8 * c8, 128);
+          *reinterpret_cast<uint4*>(sm + OFF_V + st * 16384 + o) = z;
+          for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 + o) = z;
+        }
+#pragma unroll
+        for (int c8 = 0; c8 < DK / 8; ++c8)
+          *reinterpret_cast<uint4*>(sm + OFF_K + st * 32768 + sw128_chunk(r, 8 * c8, 128)) = z;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(bar + B_VW);
+      if (!(ok = wait(B_D + 8 * st, c >> 1))) break;
+      tc_fence_after();
+#pragma unroll
+      for (int e = 0; e < BV; e += 16) {
+        float x[16], y[16], z[16];
+        tmem_ld16(row + TM_D + e, x);
+        tmem_ld16(row + TM_D + 64 + e, y);
+        tmem_ld16(row + TM_D + 128 + e, z);
+        tmem_ld_wait();
+#pragma unroll
+        for (int u = 0; u < 16; ++u) S[e + u] = fmaf(gamma, S[e + u], x[u] + (y[u] + z[u]));
+      }
+      total *= gamma;
+      if (!SUM && !(ok = wait(B_QS + 8 * st, c >> 1))) break;  // the old operand has been read
+      operand();
+      tc_fence_before();
+      mbar_arrive(bar + B_SB);
+    }
+    if (ok) {
+      if (SUM) {
+        put(p.part + (unit * p.seg_n + seg + 1) * stsz + at);
+        if (r == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = total;
+      } else if (p.Sf != nullptr && seg == p.seg_n - 1) {
+        put(p.Sf + unit * stsz + at);
+      }
+    }
+  } else if (warp < 12) {
+    // ---- out ------------------------------------------------------------------------------
+    if constexpr (!SUM) {
+      const int q4 = warp & 3;
+      const int i = tid - 256;
+      const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
+      for (int c = 0; c < nck; ++c) {
+        if (!(ok = wait(B_DEC + 8 * (c & 1), c >> 1))) break;
+        float pre = pref(c)[i];
+        for (int bk = 0; bk < q4; ++bk) pre *= tots(c)[bk];
+        mbar_arrive(bar + B_DECE + 8 * (c & 1));
+        if (!(ok = wait(B_O + 8 * (c & 1), c >> 1))) break;
+        tc_fence_after();
+        float x[BV];
+#pragma unroll
+        for (int e = 0; e < BV; e += 32) {
+          float y[32];
+          tmem_ld32(row + TM_O1 + e, y);
+          tmem_ld32(row + TM_O2 + e, x + e);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 32; ++u) x[e + u] = fmaf(pre, y[u], x[e + u]);
+        }
+        tc_fence_before();
+        mbar_arrive(bar + B_OE);
+        if (i < len_of(c)) {
+          Tout* o = static_cast<Tout*>(p.out) +
+                    ((size_t)(tok0 + (int64_t)c * C + i) * p.H + h) * p.DV + j0;
+          store_cols<BV>(o, x);
+        }
+      }
+    }
+  } else if (warp == 12) {
+    // ---- MMA ------------------------------------------------------------------------------
+    if (lane == 0) {
+      const uint64_t d_q = smem_desc(sb + OFF_Q, 16, 1024, kSwizzle128);
+      const uint64_t d_k = smem_desc(sb + OFF_K, 16, 1024, kSwizzle128);
+      const uint64_t d_km = smem_desc(sb + OFF_K, 16384, 1024, kSwizzle128);  // K^T (MN-major)
+      const uint64_t d_v = smem_desc(sb + OFF_V, 16384, 1024, kSwizzle128);
+      const uint64_t d_vw = smem_desc(sb + OFF_VW, 16384, 1024, kSwizzle128);
+      const uint64_t d_sb = smem_desc(sb + OFF_SB, 16384, 1024, kSwizzle128);
+      constexpr uint32_t id_sc = idesc_bf16(128, 128, 0, 0);
+      constexpr uint32_t id_qs = idesc_bf16(128, BV, 0, 1);
+      constexpr uint32_t id_pv = idesc_bf16(128, BV, 0, 1);
+      constexpr uint32_t id_kv = idesc_bf16(128, 3 * BV, 1, 1);
+      auto scores = [&](int c) {
+        const uint64_t so = (c & 1) ? 32768 >> 4 : 0;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint64_t ko = so + 1024 * (kk >> 2) + 2 * (kk & 3);
+          mma_f16(tmem + TM_SC, d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
+        }
+        mma_commit(bar + B_SC);
+      };
+      if constexpr (!SUM) {
+        if (nck > 0 && (ok = wait(B_Q, 0) && wait(B_K, 0))) {
+          scores(0);
+          mma_open = true; mma_off = B_SC; mma_par = 0;
+        }
+      }
+      for (int c = 0; ok && c < nck; ++c) {
+        const int st = c & 1;
+        // the state's operand is written, and the last product read
+        if (!(ok = wait(B_SB, c))) break;
+        if constexpr (!SUM) {
+          if (c > 0 && !(ok = wait(B_OE, c - 1))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16(tmem + TM_O1, d_q + (st ? 32768 >> 4 : 0) + 1024 * (kk >> 2) + 2 * (kk & 3),
+                    d_sb + 128 * kk, id_qs, kk > 0 ? 1u : 0u);
+          mma_commit(bar + B_QS + 8 * st);
+          mma_open = true; mma_off = B_QS + 8 * st; mma_par = c >> 1;
+        }
+        // (V's rows written implies V loaded; K is waited for in full here)
+        if (!(ok = wait(B_VW, c) && wait(B_K + 8 * st, c >> 1))) break;
+        tc_fence_after();
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16(tmem + TM_D, d_km + (st ? 32768 >> 4 : 0) + 128 * kk, d_vw + 128 * kk, id_kv,
+                  kk > 0 ? 1u : 0u);
+        mma_commit(bar + B_D + 8 * st);
+        mma_open = true; mma_off = B_D + 8 * st; mma_par = c >> 1;
+        if constexpr (!SUM) {
+          if (!(ok = wait(B_P, c))) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts(tmem + TM_O2, tmem + TM_P + 8 * kk, d_v + (st ? 16384 >> 4 : 0) + 128 * kk,
+                       id_pv, kk > 0 ? 1u : 0u);
+          mma_commit(bar + B_O + 8 * st);
+          mma_off = B_O + 8 * st;
+          if (c + 1 < nck) {
+            if (!(ok = wait(B_Q + 8 * (st ^ 1), (c + 1) >> 1) &&
+                       wait(B_K + 8 * (st ^ 1), (c + 1) >> 1)))
+              break;
+            scores(c + 1);
+            mma_off = B_SC; mma_par = c + 1;
+          }
+        }
+      }
+    }
+  } else if (warp == 13) {
+    // ---- loads ----------------------------------------------------------------------------
+    if (lane == 0) {
+      auto issued = [&](int kind, int c) {
+        const uint32_t bit = 1u << (2 * kind + (c & 1));
+        pend |= bit;
+        pend_par = (c >> 1 & 1) ? pend_par | bit : pend_par & ~bit;
+      };
+      auto tok = [&](int c) { return (int)(tok0 + (int64_t)c * C); };
+      auto load_q = [&](int c) {
+        const uint32_t bq = bar + B_Q + 8 * (c & 1), dst = sb + OFF_Q + (c & 1) * 32768;
+        mbar_expect_tx(bq, 32768);
+        tma_load_2d(dst, &tm_q, h * DK, tok(c), bq);
+        tma_load_2d(dst + 16384, &tm_q, h * DK + 64, tok(c), bq);
+        issued(0, c);
+      };
+      auto load_k = [&](int c) {
+        const uint32_t bk = bar + B_K + 8 * (c & 1), dst = sb + OFF_K + (c & 1) * 32768;
+        mbar_expect_tx(bk, 32768);
+        tma_load_2d(dst, &tm_k, h * DK, tok(c), bk);
+        tma_load_2d(dst + 16384, &tm_k, h * DK + 64, tok(c), bk);
+        issued(1, c);
+      };
+      auto load_v = [&](int c) {
+        const uint32_t bv = bar + B_V + 8 * (c & 1);
+        mbar_expect_tx(bv, 16384);
+        tma_load_2d(sb + OFF_V + (c & 1) * 16384, &tm_v, h * p.DV + j0, tok(c), bv);
+        issued(2, c);
+      };
+      int c = 0;
+      for (; c < 2 && c < nck; ++c) {
+        if (!SUM) load_q(c);
+        load_k(c);
+        load_v(c);
+      }
+      // chunk c takes the stage of chunk c - 2 as its parts become free
+      for (; c < nck; ++c) {
+        if constexpr (!SUM) {
+          if (!(ok = wait(B_QS + 8 * (c & 1), (c >> 1) - 1))) break;
+          load_q(c);
+        }
+        if (!(ok = wait(B_D + 8 * (c & 1), (c >> 1) - 1))) break;
+        load_k(c);
+        if (!SUM && !(ok = wait(B_O + 8 * (c & 1), (c >> 1) - 1))) break;
+        load_v(c);
+      }
+      if (!ok) {
+        // give the loads in flight their time before the block leaves
+        for (int s = 0; s < 6; ++s)
+          if (pend >> s & 1u) mbar_wait_bounded(bar + 8 * s, pend_par >> s & 1u, kWaitNs);
+      }
+    }
+  } else {
+    // ---- decays ---------------------------------------------------------------------------
+    auto load = [&](int c, float* a) {
+      const int len = c < nck ? len_of(c) : 0;
+#pragma unroll
+      for (int bk = 0; bk < 4; ++bk) {
+        const int t = 32 * bk + lane;
+        a[bk] = t < len ? p.al.at(tok0 + (int64_t)c * C + t, h) : 1.f;
+      }
+    };
+    float a[4], nx[4];
+    load(0, a);
+    for (int c = 0; c < nck; ++c) {
+      load(c + 1, nx);
+      if (c >= 2 && !(ok = wait(B_DECE + 8 * (c & 1), (c >> 1) - 1))) break;
+      float* o = reinterpret_cast<float*>(sm + OFF_DEC) + (c & 1) * (kDecBytes / 4);
+#pragma unroll
+      for (int bk = 0; bk < 4; ++bk) {
+        const float pw = warp_prefix(a[bk], lane), sw = warp_suffix(a[bk], lane);
+        o[32 * bk + lane] = pw;
+        o[128 + 32 * bk + lane] = sw;
+        if (lane == 31) o[256 + bk] = pw;
+        a[bk] = nx[bk];
+      }
+      mbar_arrive(bar + B_DEC + 8 * (c & 1));
+    }
+  }
+  if (!ok) {
+    set_status(p.status, CKDA_ERR_DEVICE_TIMEOUT);
+    if (mma_open) mbar_wait_bounded(bar + mma_off, mma_par & 1u, kWaitNs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace fw
+
+// Segments per sequence: as many as fill the SMs once, when whole sequences
+// leave half of them or more without a CTA, and each keeps 8 chunks.
+static int fwd_segments(int n_seqs, int T, int H, int dv, bool varlen) {
+  const int64_t ctas = (int64_t)n_seqs * H * (dv / fw::BV);
+  int64_t g = 148 / (ctas > 0 ? ctas : 1);
+  const int64_t most = (int64_t)T / (n_seqs > 0 && varlen ? n_seqs : 1) / (8 * fw::C);
+  if (g > most) g = most;
+  return g < 1 ? 1 : (int)g;
+}
+
+}  // namespace la
+
+bool la_fwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen) {
+  const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
+  return dtype == CKDA_BF16 && dk == la::fw::DK && (dv == 64 || dv == 128) && rows > 0 &&
+         rows <= 0x7fffffffull - la::fw::C &&
+         (uint64_t)H * (dk > dv ? dk : dv) <= 0x7fffffffull;
+}
+
+size_t la_fwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen) {
+  const int g = la::fwd_segments(n_seqs, T, H, dv, varlen);
+  return g > 1 ? (size_t)n_seqs * H * g * ((size_t)dk * dv + 64) * 4 : 0;
+}
+
+cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const void* k,
+                             const void* v, const float* alpha, int per_head, const float* S0,
+                             const int32_t* cu, void* out, float* S_final, void* ws, int n_seqs,
+                             int T, int H, int* status, cudaStream_t stream) {
+  using namespace la;
+  const bool varlen = cu != nullptr;
+  const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
+  CUtensorMap mq, mk, mv;
+  if (!bf16_map(&mq, q, (uint64_t)H * dk, rows, fw::C) ||
+      !bf16_map(&mk, k, (uint64_t)H * dk, rows, fw::C) ||
+      !bf16_map(&mv, v, (uint64_t)H * dv, rows, fw::C))
+    return cudaErrorInvalidValue;
+  const int g = fwd_segments(n_seqs, T, H, dv, varlen);
+  fw::Args a{{alpha, H, per_head}, S0, cu, out, S_final, n_seqs, T, H, dv, status, g, nullptr,
+             nullptr};
+  const unsigned units = (unsigned)n_seqs * H * (dv / fw::BV);
+  cudaError_t e;
+  if (g > 1) {
+    a.part = static_cast<float*>(ws);
+    a.dec = a.part + (size_t)n_seqs * H * g * dk * dv;
+    auto ks = fw::la_fwd_kernel<float, true>;
+    if ((e = max_smem<0>(ks, fw::kSmem)) != cudaSuccess) return e;
+    ks<<<units * (g - 1), fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (out_dtype == CKDA_BF16) {
+    auto kb = fw::la_fwd_kernel<__nv_bfloat16, false>;
+    if ((e = max_smem<1>(kb, fw::kSmem)) != cudaSuccess) return e;
+    kb<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, a);
+  } else {
+    auto kf = fw::la_fwd_kernel<float, false>;
+    if ((e = max_smem<2>(kf, fw::kSmem)) != cudaSuccess) return e;
+    kf<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace ckda

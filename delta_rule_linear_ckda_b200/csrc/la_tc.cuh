@@ -1,0 +1,135 @@
+// Pieces shared by the tensor-core kernels of head-decay linear attention.
+#pragma once
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+
+#include "la_common.cuh"
+#include "sm100.cuh"
+
+namespace ckda {
+namespace la {
+
+// The sequence of rank z by decreasing length (see seq_longest_first), with
+// the result passed on through `pick` in the caller's shared memory.
+__device__ __forceinline__ int longest_first(const int32_t* cu, int n_seqs, int z, int* pick) {
+  if (cu == nullptr || n_seqs > kLongestFirstMaxSeqs) return z;
+  if (threadIdx.x == 0) *pick = z;
+  __syncthreads();
+  for (int n = threadIdx.x; n < n_seqs; n += blockDim.x) {
+    const int ln = cu[n + 1] - cu[n];
+    int rank = 0;
+    for (int m = 0; m < n_seqs; ++m) {
+      const int lm = cu[m + 1] - cu[m];
+      rank += (lm > ln || (lm == ln && m < n)) ? 1 : 0;
+    }
+    if (rank == z) *pick = n;
+  }
+  __syncthreads();
+  return *pick;
+}
+
+// Products over a warp's lanes: through this lane, and behind it.
+__device__ __forceinline__ float warp_prefix(float a, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float b = __shfl_up_sync(0xffffffffu, a, o);
+    a = lane >= o ? a * b : a;
+  }
+  return a;
+}
+
+__device__ __forceinline__ float warp_suffix(float a, int lane) {
+  float s = __shfl_down_sync(0xffffffffu, a, 1);
+  s = lane == 31 ? 1.f : s;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float b = __shfl_down_sync(0xffffffffu, s, o);
+    s = lane + o < 32 ? s * b : s;
+  }
+  return s;
+}
+
+__device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
+__device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
+
+// A pair of fp32 values as the sum of three bf16 values each: 24 bits.
+__device__ __forceinline__ void split3f(float a, float b, uint32_t* t1, uint32_t* t2,
+                                        uint32_t* t3) {
+  *t1 = sm100::pack_bf16x2(a, b);
+  a -= lo_f(*t1);
+  b -= hi_f(*t1);
+  *t2 = sm100::pack_bf16x2(a, b);
+  a -= lo_f(*t2);
+  b -= hi_f(*t2);
+  *t3 = sm100::pack_bf16x2(a, b);
+}
+
+// A pair of bf16 values times w, split.
+__device__ __forceinline__ void split3(uint32_t in, float w, uint32_t* t1, uint32_t* t2,
+                                       uint32_t* t3) {
+  split3f(lo_f(in) * w, hi_f(in) * w, t1, t2, t3);
+}
+
+template <int N>
+__device__ __forceinline__ void store_cols(__nv_bfloat16* o, const float* x) {
+#pragma unroll
+  for (int e = 0; e < N; e += 8)
+    *reinterpret_cast<uint4*>(o + e) = make_uint4(
+        sm100::pack_bf16x2(x[e], x[e + 1]), sm100::pack_bf16x2(x[e + 2], x[e + 3]),
+        sm100::pack_bf16x2(x[e + 4], x[e + 5]), sm100::pack_bf16x2(x[e + 6], x[e + 7]));
+}
+
+template <int N>
+__device__ __forceinline__ void store_cols(float* o, const float* x) {
+#pragma unroll
+  for (int e = 0; e < N; e += 4)
+    *reinterpret_cast<float4*>(o + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+}
+
+// ---- host side ---------------------------------------------------------------------
+
+// A [rows, cols] bf16 tensor in boxes of `box_rows` x 64, 128-byte swizzle.
+inline bool bf16_map(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows,
+                     uint32_t box_rows) {
+  static std::atomic<PFN_cuTensorMapEncodeTiled_v12000> fn{nullptr};
+  auto f = fn.load(std::memory_order_acquire);
+  if (f == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) !=
+            cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    f = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    fn.store(f, std::memory_order_release);
+  }
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {cols * 2};
+  cuuint32_t box[2] = {64, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return f(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(ptr), dims, strides, box, estr,
+           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Allows kernel `id` its dynamic shared memory, once per device.
+template <int id, typename K>
+inline cudaError_t max_smem(K kern, size_t bytes) {
+  constexpr int kMaxDevices = 64;
+  static std::atomic<bool> done[kMaxDevices];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < kMaxDevices && done[dev].load(std::memory_order_acquire))
+    return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices)
+    done[dev].store(true, std::memory_order_release);
+  return e;
+}
+
+}  // namespace la
+}  // namespace ckda

@@ -160,6 +160,23 @@ def test_step(ck, dk, dv, B, H, dtype):
         la_ref.check(S, rS, tS, "S")
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_few_heads_and_long_sequences(ck, dtype):
+    """Lengths that a tensor-core call splits into segments; S_final over S0."""
+    for B, T, H, dv, lens in ((1, 4500, 2, 128, None), (2, 2200, 1, 64, None),
+                              (3, 5000, 1, 128, [1, 4980, 19])):
+        lead, cu = (B, T), None
+        if lens:
+            lead, cu = (T,), torch.tensor([0] + lens, device=DEV).cumsum(0).to(torch.int32)
+        for decay in ("signed", "one"):
+            q, k, v, a, _, S0, _ = make(lead, H, 128, dv, dtype, decay, seed=T, n=B)
+            check_fwd(ck, q, k, v, a, S0, cu)
+            o, S = ck.la_fwd_chunked(q, k, v, a, S0=S0, cu_seqlens=cu)
+            Sio = S0.clone()
+            o2, _ = ck.la_fwd_chunked(q, k, v, a, S0=Sio, S_final=Sio, cu_seqlens=cu)
+            assert torch.equal(o, o2) and torch.equal(S, Sio)
+
+
 def test_training_sizes_on_sampled_heads(ck):
     B, T, H = 4, 4096, 16
     q, k, v, a, dO, _, _ = make((B, T), H, 128, 128, torch.bfloat16, seed=8, states=False)
