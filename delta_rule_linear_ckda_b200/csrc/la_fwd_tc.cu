@@ -12,15 +12,15 @@
 // (the slices of a head read the same q and k at about the same time, from L2
 // but once).  Its warps have fixed roles and pass each chunk on through
 // mbarriers:
-//   warps 0..3   scores: tensor memory -> times the decays, masked -> bf16
-//                operand back in tensor memory (thread = row i)
-//   warps 4..7   state: V's rows times suf as bf16 operands in shared memory;
+//   warps 0..7   scores: tensor memory -> times the decays, masked -> bf16
+//                operand in the same place; out: pre_i (Q S) + (P V), stored
+//                (thread = row i; two warps share the columns of 32 rows)
+//   warps 8..15  state: V's rows times suf as bf16 operands in shared memory;
 //                S' = gamma S + product, in fp32 registers (thread = row of
-//                d_k), its bf16 copy for the next chunk
-//   warps 8..11  out: pre_i (Q S) + (P V), rounded and stored
-//   warp 12      every MMA (one thread)
-//   warp 13      every TMA load (one thread): q, k, v two chunks deep
-//   warp 14      the decays' products of each chunk
+//                d_k, half of the columns), its bf16 copy for the next chunk
+//   warp 16      every MMA (one lane issues)
+//   warp 17      every TMA load (one thread): q, k, v two chunks deep
+//   warp 18      the decays' products of each chunk
 //
 // Decays are running products within aligned blocks of 32 tokens: prefW_i
 // from the block's start through i, sufW_j from j + 1 to the block's end,
@@ -31,10 +31,9 @@
 // Roundings: the scores (after their decays) and the state's copy that the
 // queries read are rounded once to bf16, like the inputs; both only reach
 // out.  The state itself stays at fp32 accuracy: diag(suf) V is split into
-// three bf16 terms (24 bits), whose products with the exact bf16 K are one
-// MMA with the three terms side by side (N = 192).  Side by side they also
-// read K from shared memory once instead of three times; with N = 64 the
-// product would be bound by that read.
+// three bf16 terms (24 bits) whose products with the exact bf16 K are summed:
+// two terms side by side in one MMA (N = 128), which reads K from shared
+// memory once for both, and the third on top of the second.
 //
 // A sequence may be split into segments that run at the same time (few
 // sequences and heads): a first launch computes each segment's own end state
@@ -65,15 +64,16 @@ constexpr uint32_t OFF_SB = OFF_VW + 3 * 16384;  // bf16 state [128][64]
 constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x {prefW[128], sufW[128], tot[4]} fp32
 constexpr uint32_t kDecBytes = 1024 + 16;
 constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
-constexpr uint32_t OFF_MISC = OFF_BAR + 176;     // tensor-memory base, the sequence
+constexpr uint32_t OFF_MISC = OFF_BAR + 224;     // tensor-memory base, the sequence
 constexpr uint32_t kSmem = OFF_MISC + 16;
 static_assert(kSmem <= 232448, "shared memory");
 
 // mbarriers, byte offsets from OFF_BAR; each completes once per chunk (those
 // with two stages once per two)
 constexpr uint32_t B_Q = 0, B_K = 16, B_V = 32;  // stage loaded, + 8 (c & 1)
-constexpr uint32_t B_SC = 48;    // Q K^T complete (tensor core); then P's buffer is free too
-constexpr uint32_t B_P = 56;     // scores read, P written
+constexpr uint32_t B_SC = 168;   // Q K^T complete (tensor core), + 8 (c & 1)
+constexpr uint32_t B_PP = 184;   // scores read by both warps of 32 rows, + 8 (row block)
+constexpr uint32_t B_P = 48;     // P written, + 8 (c & 1): the scores run a chunk ahead
 constexpr uint32_t B_VW = 64;    // diag(suf) V written, V's and K's tail rows cleared
 constexpr uint32_t B_SB = 72;    // the state's operand written, the product read
 constexpr uint32_t B_OE = 80;    // Q S and P V read
@@ -86,14 +86,14 @@ constexpr uint32_t B_DEC = 136;  // decays of a chunk written, + 8 (c & 1)
 constexpr uint32_t B_DECE = 152; // and read, + 8 (c & 1)
 
 // tensor-memory columns
-constexpr uint32_t TM_SC = 0;    // Q K^T
-constexpr uint32_t TM_P = 128;   // P, bf16 pairs
-constexpr uint32_t TM_O1 = 192;  // Q S
-constexpr uint32_t TM_O2 = 256;  // P V
-constexpr uint32_t TM_D = 320;   // K^T diag(suf) V, three terms
+constexpr uint32_t TM_SC = 0;    // Q K^T, + 128 (c & 1); P (bf16 pairs) over its first 64
+constexpr uint32_t TM_O1 = 256;  // Q S
+constexpr uint32_t TM_O2 = 320;  // P V
+constexpr uint32_t TM_D = 384;   // K^T diag(suf) V: first term, second and third
 constexpr uint32_t kTmemCols = 512;
 
-constexpr int kThreads = 480;
+constexpr int kThreads = 608;
+constexpr int kHalf = BV / 2;  // columns per state or output thread
 
 struct Args {
   Decay al;
@@ -143,17 +143,18 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   const uint32_t bar = sb + OFF_BAR;
   if (tid == 0) {
     for (int i = 0; i < 6; ++i) mbar_init(bar + 8 * i, 1);
-    mbar_init(bar + B_SC, 1);
-    mbar_init(bar + B_P, 128);
-    mbar_init(bar + B_VW, 128);
-    mbar_init(bar + B_SB, 128);
-    mbar_init(bar + B_OE, 128);
+    mbar_init(bar + B_VW, 8);
+    mbar_init(bar + B_SB, 8);
+    mbar_init(bar + B_OE, 8);
+    for (int i = 0; i < 4; ++i) mbar_init(bar + B_PP + 8 * i, 2);
     for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + B_SC + 8 * i, 1);
+      mbar_init(bar + B_P + 8 * i, 8);
       mbar_init(bar + B_D + 8 * i, 1);
       mbar_init(bar + B_QS + 8 * i, 1);
       mbar_init(bar + B_O + 8 * i, 1);
-      mbar_init(bar + B_DEC + 8 * i, 32);
-      mbar_init(bar + B_DECE + 8 * i, SUM ? 128 : 384);
+      mbar_init(bar + B_DEC + 8 * i, 1);
+      mbar_init(bar + B_DECE + 8 * i, SUM ? 8 : 16);
     }
     fence_mbar_init();
     prefetch_tmap(&tm_q);
@@ -184,87 +185,137 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   auto pref = [&](int c) { return dec0 + (c & 1) * (kDecBytes / 4); };
   auto suff = [&](int c) { return pref(c) + 128; };
   auto tots = [&](int c) { return pref(c) + 256; };
+  // One arrival per warp, once all of its lanes are here: a lane's arrivals
+  // on one mbarrier follow each other, 256 of them take some 500 cycles.
+  auto arrive = [&](uint32_t off) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + off);
+  };
   bool ok = true;
   // the copy thread's loads, bit 2 (Q, K, V) + stage: issued, and the parity of the last one
   uint32_t pend = 0, pend_par = 0;
   bool mma_open = false;
   uint32_t mma_off = 0, mma_par = 0;
 
-  if (warp < 4) {
-    // ---- scores ---------------------------------------------------------------------------
+  if (warp < 8) {
+    // ---- scores and out ---------------------------------------------------------------------
     if constexpr (!SUM) {
-      const int i = tid;  // row
-      const uint32_t row = tmem + ((uint32_t)(32 * warp) << 16);
-      {
-        // blocks right of the diagonal stay zero
-        uint32_t z[16];
-#pragma unroll
-        for (int e = 0; e < 16; ++e) z[e] = 0u;
-        for (int J = warp + 1; J < 4; ++J) tmem_st16(row + TM_P + 16 * J, z);
-        tmem_st_wait();
-      }
+      const int w4 = warp & 3, hf = warp >> 2;  // row block; which of its two warps
+      const int i = 32 * w4 + lane;             // row
+      const uint32_t row = tmem + ((uint32_t)(32 * w4) << 16);
+      // 32-column blocks of the scores: the first warp takes the diagonal one
+      // (and, of the last rows, block 0), the second those left of it
+      const bool has0 = hf == 0 || w4 >= 1, has1 = hf == 0 ? w4 == 3 : w4 >= 2;
+      const int J0 = hf == 0 ? w4 : w4 - 1, J1 = hf == 0 ? 0 : w4 - 2;
       auto load_a = [&](int c) -> float {
-        return (c < nck && i < len_of(c)) ? p.al.at(tok0 + (int64_t)c * C + i, h) : 1.f;
+        return (hf == 0 && c < nck && i < len_of(c)) ? p.al.at(tok0 + (int64_t)c * C + i, h) : 1.f;
       };
-      float a = load_a(0);
+      float a = load_a(0), pre = 0.f;
+      auto out = [&](int c) -> bool {
+        if (!wait(B_O + 8 * (c & 1), c >> 1)) return false;
+        tc_fence_after();
+        float x[kHalf];
+        tmem_ld32(row + TM_O2 + kHalf * hf, x);
+#pragma unroll
+        for (int e = 0; e < kHalf; e += 16) {
+          float y[16];
+          tmem_ld16(row + TM_O1 + kHalf * hf + e, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 16; ++u) x[e + u] = fmaf(pre, y[u], x[e + u]);
+        }
+        tc_fence_before();
+        arrive(B_OE);
+        if (i < len_of(c))
+          store_cols<kHalf>(static_cast<Tout*>(p.out) +
+                                ((size_t)(tok0 + (int64_t)c * C + i) * p.H + h) * p.DV + j0 +
+                                kHalf * hf,
+                            x);
+        return true;
+      };
       for (int c = 0; c < nck; ++c) {
         const float a_next = load_a(c + 1);
         if (!(ok = wait(B_DEC + 8 * (c & 1), c >> 1))) break;
         const float* sw = suff(c);
         const float* tot = tots(c);
-        float d = pref(c)[i];  // times the blocks between, going left
-        if (!(ok = wait(B_SC, c))) break;
+        const float pw = pref(c)[i];
+        const float tot0 = tot[0], tot1 = tot[1], tot2 = tot[2];
+        // the decays between block J and this row's
+        float d0 = pw, d1 = pw;
+        if (hf == 0) {
+          if (w4 == 3) d1 *= tot1 * tot2;
+        } else {
+          d1 *= w4 == 2 ? tot1 : tot2;
+        }
+        if (!(ok = wait(B_SC + 8 * (c & 1), c >> 1))) break;
         tc_fence_after();
-        float s[32];
-        uint32_t w[16];
-        // the diagonal block: D(i, j) runs down from 1 at j = i
-        tmem_ld32(row + TM_SC + 32 * warp, s);
-        tmem_ld_wait();
-        {
-          float run = 1.f;
+        const uint32_t sc = row + TM_SC + 128 * (c & 1);
+        uint32_t w0[16], w1[16];
+        auto decay = [&](int J, float d, uint32_t* w) {
+          float s[32];
+          tmem_ld32(sc + 32 * J, s);
+          tmem_ld_wait();
+          const float* x = sw + 32 * J;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 f = *reinterpret_cast<const float4*>(x + 4 * e);
+            w[2 * e] = pack_bf16x2(s[4 * e] * (d * f.x), s[4 * e + 1] * (d * f.y));
+            w[2 * e + 1] = pack_bf16x2(s[4 * e + 2] * (d * f.z), s[4 * e + 3] * (d * f.w));
+          }
+        };
+        if (hf == 0) {
+          // the diagonal block: D(i, j) runs down from 1 at j = i
+          float s0[32], run = 1.f;
+          tmem_ld32(sc + 32 * J0, s0);
+          tmem_ld_wait();
 #pragma unroll
           for (int j = 31; j >= 0; --j) {
             const float aj = __shfl_sync(0xffffffffu, a, j);
-            s[j] = j <= lane ? s[j] * run : 0.f;
+            s0[j] = j <= lane ? s0[j] * run : 0.f;
             run = j <= lane ? run * aj : run;
           }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) w0[e] = pack_bf16x2(s0[2 * e], s0[2 * e + 1]);
+        } else if (has0) {
+          decay(J0, d0, w0);
         }
+        if (has1) decay(J1, d1, w1);
+        tc_fence_before();
+        arrive(B_PP + 8 * w4);
+        // P lies over scores that the other warp reads
+        if (!(ok = wait(B_PP + 8 * w4, c))) break;
+        tc_fence_after();
+        if (has0) tmem_st16(sc + 16 * J0, w0);
+        if (has1) tmem_st16(sc + 16 * J1, w1);
+        if (hf == 1) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
-        tmem_st16(row + TM_P + 16 * warp, w);
-        for (int J = warp - 1; J >= 0; --J) {
-          tmem_ld32(row + TM_SC + 32 * J, s);
-          tmem_ld_wait();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 x = *reinterpret_cast<const float4*>(sw + 32 * J + 4 * e);
-            w[2 * e] = pack_bf16x2(s[4 * e] * (d * x.x), s[4 * e + 1] * (d * x.y));
-            w[2 * e + 1] = pack_bf16x2(s[4 * e + 2] * (d * x.z), s[4 * e + 3] * (d * x.w));
-          }
-          tmem_st16(row + TM_P + 16 * J, w);
-          d *= tot[J];
+          for (int e = 0; e < 16; ++e) w0[e] = 0u;
+          for (int J = w4 + 1; J < 4; ++J) tmem_st16(sc + 16 * J, w0);
         }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(bar + B_P);
-        mbar_arrive(bar + B_DECE + 8 * (c & 1));
+        arrive(B_P + 8 * (c & 1));
+        arrive(B_DECE + 8 * (c & 1));
+        if (c > 0 && !(ok = out(c - 1))) break;
+        pre = pw * (w4 > 0 ? tot0 : 1.f) * (w4 > 1 ? tot1 : 1.f) * (w4 > 2 ? tot2 : 1.f);
         a = a_next;
       }
+      if (ok && nck > 0) ok = out(nck - 1);
     }
-  } else if (warp < 8) {
+  } else if (warp < 16) {
     // ---- state ----------------------------------------------------------------------------
-    const int q4 = warp & 3;
-    const int r = tid - 128;  // token j of V, row i of the state
+    const int q4 = warp & 3, hf = (warp >> 2) & 1;
+    const int r = 32 * q4 + lane;  // token j of V, row i of the state
     const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
-    float S[BV];
+    float S[kHalf];
 #pragma unroll
-    for (int e = 0; e < BV; ++e) S[e] = 0.f;
+    for (int e = 0; e < kHalf; ++e) S[e] = 0.f;
     const size_t unit = (size_t)n * p.H + h;
-    const size_t at = ((size_t)r * p.DV) + j0;  // this row's columns in a state
+    const size_t at = ((size_t)r * p.DV) + j0 + kHalf * hf;  // this thread's columns of a state
     const size_t stsz = (size_t)DK * p.DV;
     auto add = [&](const float* src, float f) {
 #pragma unroll
-      for (int e = 0; e < BV; e += 4) {
+      for (int e = 0; e < kHalf; e += 4) {
         const float4 x = *reinterpret_cast<const float4*>(src + e);
         S[e] = fmaf(f, x.x, S[e]);
         S[e + 1] = fmaf(f, x.y, S[e + 1]);
@@ -272,22 +323,16 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         S[e + 3] = fmaf(f, x.w, S[e + 3]);
       }
     };
-    auto put = [&](float* dst) {
-#pragma unroll
-      for (int e = 0; e < BV; e += 4)
-        *reinterpret_cast<float4*>(dst + e) = make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
-    };
     if (seg == 0) {
       // (with segments the last one may write S_final over S0 before this
       // block starts: the first launch keeps a copy)
-      const float* s0 = p.S0;
-      if (s0 != nullptr) {
+      if (p.S0 != nullptr) {
         if (!SUM && p.seg_n > 1)
           add(p.part + unit * p.seg_n * stsz + at, 1.f);
         else
-          add(s0 + unit * stsz + at, 1.f);
+          add(p.S0 + unit * stsz + at, 1.f);
       }
-      if (SUM && s0 != nullptr) put(p.part + unit * p.seg_n * stsz + at);
+      if (SUM && p.S0 != nullptr) store_cols<kHalf>(p.part + unit * p.seg_n * stsz + at, S);
     } else if (!SUM) {
       float f = 1.f;
       for (int g = seg; g >= 1; --g) {
@@ -298,9 +343,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     auto operand = [&]() {
       if constexpr (!SUM) {
 #pragma unroll
-        for (int c8 = 0; c8 < BV / 8; ++c8) {
+        for (int c8 = 0; c8 < kHalf / 8; ++c8) {
           const float* x = S + 8 * c8;
-          *reinterpret_cast<uint4*>(sm + OFF_SB + sw128_chunk(r, 8 * c8, 128)) =
+          *reinterpret_cast<uint4*>(sm + OFF_SB + sw128_chunk(r, kHalf * hf + 8 * c8, 128)) =
               make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
                          pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
         }
@@ -308,7 +353,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       }
     };
     operand();
-    mbar_arrive(bar + B_SB);
+    arrive(B_SB);
     float total = 1.f;
     for (int c = 0; c < nck; ++c) {
       const int st = c & 1;
@@ -318,18 +363,21 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       float wgt = suff(c)[r];
       for (int bk = q4 + 1; bk < 4; ++bk) wgt *= tot[bk];
       const float gamma = (tot[0] * tot[1]) * (tot[2] * tot[3]);
-      mbar_arrive(bar + B_DECE + 8 * st);
+      arrive(B_DECE + 8 * st);
       if (!(ok = wait(B_V + 8 * st, c >> 1) && (len == C || wait(B_K + 8 * st, c >> 1)))) break;
       if (r < len) {
+        uint4 raw[kHalf / 8];
 #pragma unroll
-        for (int c8 = 0; c8 < BV / 8; ++c8) {
-          const uint32_t o = sw128_chunk(r, 8 * c8, 128);
-          const uint4 raw = *reinterpret_cast<const uint4*>(sm + OFF_V + st * 16384 + o);
-          const uint32_t in[4] = {raw.x, raw.y, raw.z, raw.w};
+        for (int c8 = 0; c8 < kHalf / 8; ++c8)
+          raw[c8] = *reinterpret_cast<const uint4*>(sm + OFF_V + st * 16384 +
+                                                    sw128_chunk(r, kHalf * hf + 8 * c8, 128));
+#pragma unroll
+        for (int c8 = 0; c8 < kHalf / 8; ++c8) {
+          const uint32_t in[4] = {raw[c8].x, raw[c8].y, raw[c8].z, raw[c8].w};
           uint32_t t1[4], t2[4], t3[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) split3(in[e], wgt, &t1[e], &t2[e], &t3[e]);
-          uint8_t* d = sm + OFF_VW + o;
+          uint8_t* d = sm + OFF_VW + sw128_chunk(r, kHalf * hf + 8 * c8, 128);
           *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
           *reinterpret_cast<uint4*>(d + 16384) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
           *reinterpret_cast<uint4*>(d + 32768) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
@@ -338,148 +386,129 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         // past the sequence's end lie other tokens, or none: V and K rows
         // cleared, so that no product meets what is not finite there
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int c8 = 0; c8 < BV / 8; ++c8) {
-          const uint32_t o = sw128_chunk(r, 8 * c8, 128);
+        for (int c8 = 0; c8 < kHalf / 8; ++c8) {
+          const uint32_t o = sw128_chunk(r, kHalf * hf + 8 * c8, 128);
           *reinterpret_cast<uint4*>(sm + OFF_V + st * 16384 + o) = z;
           for (int e = 0; e < 3; ++e)
             *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 + o) = z;
         }
-#pragma unroll
-        for (int c8 = 0; c8 < DK / 8; ++c8)
-          *reinterpret_cast<uint4*>(sm + OFF_K + st * 32768 + sw128_chunk(r, 8 * c8, 128)) = z;
+        for (int c8 = 0; c8 < DK / 16; ++c8)
+          *reinterpret_cast<uint4*>(sm + OFF_K + st * 32768 +
+                                    sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar + B_VW);
+      arrive(B_VW);
       if (!(ok = wait(B_D + 8 * st, c >> 1))) break;
       tc_fence_after();
+      {
 #pragma unroll
-      for (int e = 0; e < BV; e += 16) {
-        float x[16], y[16], z[16];
-        tmem_ld16(row + TM_D + e, x);
-        tmem_ld16(row + TM_D + 64 + e, y);
-        tmem_ld16(row + TM_D + 128 + e, z);
-        tmem_ld_wait();
+        for (int e = 0; e < kHalf; e += 16) {
+          float x[16], y[16];
+          tmem_ld16(row + TM_D + kHalf * hf + e, x);
+          tmem_ld16(row + TM_D + BV + kHalf * hf + e, y);
+          tmem_ld_wait();
 #pragma unroll
-        for (int u = 0; u < 16; ++u) S[e + u] = fmaf(gamma, S[e + u], x[u] + (y[u] + z[u]));
+          for (int u = 0; u < 16; ++u) S[e + u] = fmaf(gamma, S[e + u], x[u] + y[u]);
+        }
       }
       total *= gamma;
       if (!SUM && !(ok = wait(B_QS + 8 * st, c >> 1))) break;  // the old operand has been read
       operand();
       tc_fence_before();
-      mbar_arrive(bar + B_SB);
+      arrive(B_SB);
     }
     if (ok) {
       if (SUM) {
-        put(p.part + (unit * p.seg_n + seg + 1) * stsz + at);
-        if (r == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = total;
+        store_cols<kHalf>(p.part + (unit * p.seg_n + seg + 1) * stsz + at, S);
+        if (r == 0 && hf == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = total;
       } else if (p.Sf != nullptr && seg == p.seg_n - 1) {
-        put(p.Sf + unit * stsz + at);
+        store_cols<kHalf>(p.Sf + unit * stsz + at, S);
       }
     }
-  } else if (warp < 12) {
-    // ---- out ------------------------------------------------------------------------------
-    if constexpr (!SUM) {
-      const int q4 = warp & 3;
-      const int i = tid - 256;
-      const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
-      for (int c = 0; c < nck; ++c) {
-        if (!(ok = wait(B_DEC + 8 * (c & 1), c >> 1))) break;
-        float pre = pref(c)[i];
-        for (int bk = 0; bk < q4; ++bk) pre *= tots(c)[bk];
-        mbar_arrive(bar + B_DECE + 8 * (c & 1));
-        if (!(ok = wait(B_O + 8 * (c & 1), c >> 1))) break;
-        tc_fence_after();
-        float x[BV];
-#pragma unroll
-        for (int e = 0; e < BV; e += 32) {
-          float y[32];
-          tmem_ld32(row + TM_O1 + e, y);
-          tmem_ld32(row + TM_O2 + e, x + e);
-          tmem_ld_wait();
-#pragma unroll
-          for (int u = 0; u < 32; ++u) x[e + u] = fmaf(pre, y[u], x[e + u]);
-        }
-        tc_fence_before();
-        mbar_arrive(bar + B_OE);
-        if (i < len_of(c)) {
-          Tout* o = static_cast<Tout*>(p.out) +
-                    ((size_t)(tok0 + (int64_t)c * C + i) * p.H + h) * p.DV + j0;
-          store_cols<BV>(o, x);
-        }
-      }
-    }
-  } else if (warp == 12) {
+  } else if (warp == 16) {
     // ---- MMA ------------------------------------------------------------------------------
-    if (lane == 0) {
-      const uint64_t d_q = smem_desc(sb + OFF_Q, 16, 1024, kSwizzle128);
-      const uint64_t d_k = smem_desc(sb + OFF_K, 16, 1024, kSwizzle128);
-      const uint64_t d_km = smem_desc(sb + OFF_K, 16384, 1024, kSwizzle128);  // K^T (MN-major)
-      const uint64_t d_v = smem_desc(sb + OFF_V, 16384, 1024, kSwizzle128);
-      const uint64_t d_vw = smem_desc(sb + OFF_VW, 16384, 1024, kSwizzle128);
-      const uint64_t d_sb = smem_desc(sb + OFF_SB, 16384, 1024, kSwizzle128);
-      constexpr uint32_t id_sc = idesc_bf16(128, 128, 0, 0);
-      constexpr uint32_t id_qs = idesc_bf16(128, BV, 0, 1);
-      constexpr uint32_t id_pv = idesc_bf16(128, BV, 0, 1);
-      constexpr uint32_t id_kv = idesc_bf16(128, 3 * BV, 1, 1);
-      auto scores = [&](int c) {
-        const uint64_t so = (c & 1) ? 32768 >> 4 : 0;
+    // (the whole warp waits, one lane issues)
+    const uint64_t d_q = smem_desc(sb + OFF_Q, 16, 1024, kSwizzle128);
+    const uint64_t d_k = smem_desc(sb + OFF_K, 16, 1024, kSwizzle128);
+    const uint64_t d_km = smem_desc(sb + OFF_K, 16384, 1024, kSwizzle128);  // K^T (MN-major)
+    const uint64_t d_v = smem_desc(sb + OFF_V, 16384, 1024, kSwizzle128);
+    const uint64_t d_vw = smem_desc(sb + OFF_VW, 16384, 1024, kSwizzle128);
+    const uint64_t d_sb = smem_desc(sb + OFF_SB, 16384, 1024, kSwizzle128);
+    constexpr uint32_t id_sc = idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t id_qs = idesc_bf16(128, BV, 0, 1);
+    constexpr uint32_t id_pv = idesc_bf16(128, BV, 0, 1);
+    constexpr uint32_t id_kv2 = idesc_bf16(128, 2 * BV, 1, 1), id_kv1 = idesc_bf16(128, BV, 1, 1);
+    auto scores = [&](int c) {
+      const uint64_t so = (uint64_t)(c & 1) * (32768 >> 4);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t ko = so + 1024 * (kk >> 2) + 2 * (kk & 3);
-          mma_f16(tmem + TM_SC, d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
+          mma_f16(tmem + TM_SC + 128 * (c & 1), d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
         }
-        mma_commit(bar + B_SC);
-      };
-      if constexpr (!SUM) {
-        if (nck > 0 && (ok = wait(B_Q, 0) && wait(B_K, 0))) {
-          scores(0);
-          mma_open = true; mma_off = B_SC; mma_par = 0;
-        }
+        mma_commit(bar + B_SC + 8 * (c & 1));
       }
-      for (int c = 0; ok && c < nck; ++c) {
-        const int st = c & 1;
-        // the state's operand is written, and the last product read
-        if (!(ok = wait(B_SB, c))) break;
-        if constexpr (!SUM) {
-          if (c > 0 && !(ok = wait(B_OE, c - 1))) break;
-          tc_fence_after();
+      __syncwarp();
+      mma_open = true; mma_off = B_SC + 8 * (c & 1); mma_par = c >> 1;
+    };
+    if constexpr (!SUM) {
+      if (nck > 0 && (ok = wait(B_Q, 0) && wait(B_K, 0))) scores(0);
+    }
+    for (int c = 0; ok && c < nck; ++c) {
+      const uint32_t st = c & 1;
+      const uint64_t so = (uint64_t)st * (32768 >> 4);
+      // the state's operand is written, and the last product read
+      if (!(ok = wait(B_SB, c))) break;
+      if constexpr (!SUM) {
+        if (c > 0 && !(ok = wait(B_OE, c - 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16(tmem + TM_O1, d_q + (st ? 32768 >> 4 : 0) + 1024 * (kk >> 2) + 2 * (kk & 3),
-                    d_sb + 128 * kk, id_qs, kk > 0 ? 1u : 0u);
+            mma_f16(tmem + TM_O1, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
+                    id_qs, kk > 0 ? 1u : 0u);
           mma_commit(bar + B_QS + 8 * st);
-          mma_open = true; mma_off = B_QS + 8 * st; mma_par = c >> 1;
         }
-        // (V's rows written implies V loaded; K is waited for in full here)
-        if (!(ok = wait(B_VW, c) && wait(B_K + 8 * st, c >> 1))) break;
-        tc_fence_after();
+        __syncwarp();
+        mma_open = true; mma_off = B_QS + 8 * st; mma_par = c >> 1;
+      }
+      // (V's rows written implies V loaded; K is waited for in full here)
+      if (!(ok = wait(B_VW, c) && wait(B_K + 8 * st, c >> 1))) break;
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16(tmem + TM_D, d_km + (st ? 32768 >> 4 : 0) + 128 * kk, d_vw + 128 * kk, id_kv,
-                  kk > 0 ? 1u : 0u);
+          mma_f16(tmem + TM_D, d_km + so + 128 * kk, d_vw + 128 * kk, id_kv2, kk > 0 ? 1u : 0u);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16(tmem + TM_D + BV, d_km + so + 128 * kk, d_vw + (32768 >> 4) + 128 * kk, id_kv1, 1u);
         mma_commit(bar + B_D + 8 * st);
-        mma_open = true; mma_off = B_D + 8 * st; mma_par = c >> 1;
-        if constexpr (!SUM) {
-          if (!(ok = wait(B_P, c))) break;
-          tc_fence_after();
+      }
+      __syncwarp();
+      mma_open = true; mma_off = B_D + 8 * st; mma_par = c >> 1;
+      if constexpr (!SUM) {
+        if (!(ok = wait(B_P + 8 * st, c >> 1))) break;
+        tc_fence_after();
+        if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmem + TM_O2, tmem + TM_P + 8 * kk, d_v + (st ? 16384 >> 4 : 0) + 128 * kk,
+            mma_f16_ts(tmem + TM_O2, tmem + TM_SC + 128 * st + 8 * kk, d_v + (so >> 1) + 128 * kk,
                        id_pv, kk > 0 ? 1u : 0u);
           mma_commit(bar + B_O + 8 * st);
-          mma_off = B_O + 8 * st;
-          if (c + 1 < nck) {
-            if (!(ok = wait(B_Q + 8 * (st ^ 1), (c + 1) >> 1) &&
-                       wait(B_K + 8 * (st ^ 1), (c + 1) >> 1)))
-              break;
-            scores(c + 1);
-            mma_off = B_SC; mma_par = c + 1;
-          }
+        }
+        __syncwarp();
+        mma_off = B_O + 8 * st;
+        // the next chunk's scores, last: K comes into its stage only after
+        // the last chunk's product with it, and is then still on its way
+        if (c + 1 < nck) {
+          if (!(ok = wait(B_Q + 8 * (st ^ 1), (c + 1) >> 1) &&
+                     wait(B_K + 8 * (st ^ 1), (c + 1) >> 1)))
+            break;
+          scores(c + 1);
         }
       }
     }
-  } else if (warp == 13) {
+  } else if (warp == 17) {
     // ---- loads ----------------------------------------------------------------------------
     if (lane == 0) {
       auto issued = [&](int kind, int c) {
@@ -508,12 +537,23 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tma_load_2d(sb + OFF_V + (c & 1) * 16384, &tm_v, h * p.DV + j0, tok(c), bv);
         issued(2, c);
       };
+      // into L2 two chunks ahead of the loads
+      auto prefetch = [&](int c) {
+        if (c >= nck) return;
+        for (int x = 0; x < 128; x += 64) {
+          if (!SUM) tma_prefetch_2d(&tm_q, h * DK + x, tok(c));
+          tma_prefetch_2d(&tm_k, h * DK + x, tok(c));
+        }
+        tma_prefetch_2d(&tm_v, h * p.DV + j0, tok(c));
+      };
       int c = 0;
       for (; c < 2 && c < nck; ++c) {
         if (!SUM) load_q(c);
         load_k(c);
         load_v(c);
       }
+      prefetch(2);
+      prefetch(3);
       // chunk c takes the stage of chunk c - 2 as its parts become free
       for (; c < nck; ++c) {
         if constexpr (!SUM) {
@@ -524,6 +564,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         load_k(c);
         if (!SUM && !(ok = wait(B_O + 8 * (c & 1), (c >> 1) - 1))) break;
         load_v(c);
+        prefetch(c + 2);
       }
       if (!ok) {
         // give the loads in flight their time before the block leaves
@@ -531,7 +572,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (pend >> s & 1u) mbar_wait_bounded(bar + 8 * s, pend_par >> s & 1u, kWaitNs);
       }
     }
-  } else {
+  } else if (warp == 18) {
     // ---- decays ---------------------------------------------------------------------------
     auto load = [&](int c, float* a) {
       const int len = c < nck ? len_of(c) : 0;
@@ -555,12 +596,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (lane == 31) o[256 + bk] = pw;
         a[bk] = nx[bk];
       }
-      mbar_arrive(bar + B_DEC + 8 * (c & 1));
+      arrive(B_DEC + 8 * (c & 1));
     }
   }
   if (!ok) {
     set_status(p.status, CKDA_ERR_DEVICE_TIMEOUT);
-    if (mma_open) mbar_wait_bounded(bar + mma_off, mma_par & 1u, kWaitNs);
+    if (warp == 16 && mma_open) mbar_wait_bounded(bar + mma_off, mma_par & 1u, kWaitNs);
   }
   tc_fence_before();
   __syncthreads();

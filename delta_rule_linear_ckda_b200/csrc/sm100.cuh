@@ -93,6 +93,20 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// One lane of a converged warp (the same one every time).  A branch on this
+// keeps the operands of what it guards in uniform registers; behind a branch
+// on the lane index the compiler moves each of them there by itself, about
+// 100 cycles per tcgen05.mma.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
 // Make generic-proxy shared-memory writes visible to the async proxy
 // (tensor-core operand reads, TMA), and order prior generic accesses before
 // later async-proxy writes.
