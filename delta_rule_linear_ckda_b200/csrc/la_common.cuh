@@ -16,6 +16,13 @@ struct Decay {
   __device__ __forceinline__ float at(int64_t tok, int h) const {
     return __ldg(per_head ? p + h : p + tok * H + h);
   }
+  // The same, issued where it stands: the compiler may move a plain load past
+  // waits, down to its use.
+  __device__ __forceinline__ float now(int64_t tok, int h) const {
+    float x;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(x) : "l"(per_head ? p + h : p + tok * H + h));
+    return x;
+  }
 };
 
 // Chunks of `C` tokens, numbered over the batch: a sequence's first slot.

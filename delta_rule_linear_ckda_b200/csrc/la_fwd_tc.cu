@@ -61,22 +61,24 @@ constexpr uint32_t OFF_K = 65536;                // 2 stages, the same
 constexpr uint32_t OFF_V = 131072;               // 2 stages [128][64]
 constexpr uint32_t OFF_VW = 163840;              // diag(suf) V: 3 terms [128][64]
 constexpr uint32_t OFF_SB = OFF_VW + 3 * 16384;  // bf16 state [128][64]
-constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x {prefW[128], sufW[128], tot[4]} fp32
+constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x {a[128], sufW[128], tot[4]} fp32
 constexpr uint32_t kDecBytes = 1024 + 16;
 constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
-constexpr uint32_t OFF_MISC = OFF_BAR + 224;     // tensor-memory base, the sequence
+constexpr uint32_t OFF_MISC = OFF_BAR + 256;     // tensor-memory base, the sequence
 constexpr uint32_t kSmem = OFF_MISC + 16;
 static_assert(kSmem <= 232448, "shared memory");
 
 // mbarriers, byte offsets from OFF_BAR; each completes once per chunk (those
 // with two stages once per two)
 constexpr uint32_t B_Q = 0, B_K = 16, B_V = 32;  // stage loaded, + 8 (c & 1)
-constexpr uint32_t B_SC = 168;   // Q K^T complete (tensor core), + 8 (c & 1)
+constexpr uint32_t B_SC = 168;   // Q K^T complete (tensor core)
+constexpr uint32_t B_OE = 216;   // Q S and P V read, + 8 (c & 1)
+constexpr uint32_t B_ST = 232;   // out staged where V was (or stored), + 8 (c & 1)
 constexpr uint32_t B_PP = 184;   // scores read by both warps of 32 rows, + 8 (row block)
-constexpr uint32_t B_P = 48;     // P written, + 8 (c & 1): the scores run a chunk ahead
-constexpr uint32_t B_VW = 64;    // diag(suf) V written, V's and K's tail rows cleared
-constexpr uint32_t B_SB = 72;    // the state's operand written, the product read
-constexpr uint32_t B_OE = 80;    // Q S and P V read
+constexpr uint32_t B_P = 48;     // P written
+constexpr uint32_t B_VW = 64;    // diag(suf) V written, V's and K's tail rows cleared, the last
+                                 // chunk's product read
+constexpr uint32_t B_SB = 72;    // the state's operand written
 // complete (tensor core), + 8 (c & 1): the copy thread, which nothing holds
 // to the chunk, waits for these too
 constexpr uint32_t B_D = 88;     // K^T diag(suf) V
@@ -86,9 +88,9 @@ constexpr uint32_t B_DEC = 136;  // decays of a chunk written, + 8 (c & 1)
 constexpr uint32_t B_DECE = 152; // and read, + 8 (c & 1)
 
 // tensor-memory columns
-constexpr uint32_t TM_SC = 0;    // Q K^T, + 128 (c & 1); P (bf16 pairs) over its first 64
-constexpr uint32_t TM_O1 = 256;  // Q S
-constexpr uint32_t TM_O2 = 320;  // P V
+constexpr uint32_t TM_SC = 0;    // Q K^T; P (bf16 pairs) over its first 64
+constexpr uint32_t TM_O1 = 128;  // Q S, + 128 (c & 1)
+constexpr uint32_t TM_O2 = 192;  // P V, + 128 (c & 1)
 constexpr uint32_t TM_D = 384;   // K^T diag(suf) V: first term, second and third
 constexpr uint32_t kTmemCols = 512;
 
@@ -115,7 +117,8 @@ struct Args {
 template <typename Tout, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1)
 la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v, const Args p) {
+              const __grid_constant__ CUtensorMap tm_v,
+              const __grid_constant__ CUtensorMap tm_o, const Args p) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -145,11 +148,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     for (int i = 0; i < 6; ++i) mbar_init(bar + 8 * i, 1);
     mbar_init(bar + B_VW, 8);
     mbar_init(bar + B_SB, 8);
-    mbar_init(bar + B_OE, 8);
+    mbar_init(bar + B_SC, 1);
+    mbar_init(bar + B_P, 8);
     for (int i = 0; i < 4; ++i) mbar_init(bar + B_PP + 8 * i, 2);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar + B_SC + 8 * i, 1);
-      mbar_init(bar + B_P + 8 * i, 8);
+      mbar_init(bar + B_OE + 8 * i, 8);
+      mbar_init(bar + B_ST + 8 * i, 8);
       mbar_init(bar + B_D + 8 * i, 1);
       mbar_init(bar + B_QS + 8 * i, 1);
       mbar_init(bar + B_O + 8 * i, 1);
@@ -160,6 +164,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    if (!SUM) prefetch_tmap(&tm_o);
   }
   if (warp == 0) {
     tmem_alloc(sb + OFF_MISC, kTmemCols);
@@ -182,9 +187,13 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     return mbar_wait_bounded(bar + off, par & 1u, kWaitNs);
   };
   const float* dec0 = reinterpret_cast<const float*>(sm + OFF_DEC);
-  auto pref = [&](int c) { return dec0 + (c & 1) * (kDecBytes / 4); };
-  auto suff = [&](int c) { return pref(c) + 128; };
-  auto tots = [&](int c) { return pref(c) + 256; };
+  auto decs = [&](int c) { return dec0 + (c & 1) * (kDecBytes / 4); };
+  auto suff = [&](int c) { return decs(c) + 128; };
+  auto tots = [&](int c) { return decs(c) + 256; };
+  // Whole chunks of bf16 leave by TMA from the V tile, which the products are
+  // done with by then: a thread's own row would be four stores to 32 different
+  // lines per warp, and 1024 cycles of the load / store unit per chunk.
+  auto staged = [&](int c) -> bool { return sizeof(Tout) == 2 && len_of(c) == C; };
   // One arrival per warp, once all of its lanes are here: a lane's arrivals
   // on one mbarrier follow each other, 256 of them take some 500 cycles.
   auto arrive = [&](uint32_t off) {
@@ -207,38 +216,48 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // (and, of the last rows, block 0), the second those left of it
       const bool has0 = hf == 0 || w4 >= 1, has1 = hf == 0 ? w4 == 3 : w4 >= 2;
       const int J0 = hf == 0 ? w4 : w4 - 1, J1 = hf == 0 ? 0 : w4 - 2;
-      auto load_a = [&](int c) -> float {
-        return (hf == 0 && c < nck && i < len_of(c)) ? p.al.at(tok0 + (int64_t)c * C + i, h) : 1.f;
-      };
-      float a = load_a(0), pre = 0.f;
+      float pre = 0.f;
       auto out = [&](int c) -> bool {
         if (!wait(B_O + 8 * (c & 1), c >> 1)) return false;
         tc_fence_after();
         float x[kHalf];
-        tmem_ld32(row + TM_O2 + kHalf * hf, x);
+        tmem_ld32(row + TM_O2 + 128 * (c & 1) + kHalf * hf, x);
 #pragma unroll
         for (int e = 0; e < kHalf; e += 16) {
           float y[16];
-          tmem_ld16(row + TM_O1 + kHalf * hf + e, y);
+          tmem_ld16(row + TM_O1 + 128 * (c & 1) + kHalf * hf + e, y);
           tmem_ld_wait();
 #pragma unroll
           for (int u = 0; u < 16; ++u) x[e + u] = fmaf(pre, y[u], x[e + u]);
         }
         tc_fence_before();
-        arrive(B_OE);
-        if (i < len_of(c))
+        arrive(B_OE + 8 * (c & 1));
+        if (staged(c)) {
+#pragma unroll
+          for (int c8 = 0; c8 < kHalf / 8; ++c8) {
+            const float* y = x + 8 * c8;
+            *reinterpret_cast<uint4*>(sm + OFF_V + (c & 1) * 16384 +
+                                      sw128_chunk(i, kHalf * hf + 8 * c8, 128)) =
+                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
+                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+          }
+          fence_proxy_async_smem();
+        } else if (i < len_of(c)) {
           store_cols<kHalf>(static_cast<Tout*>(p.out) +
                                 ((size_t)(tok0 + (int64_t)c * C + i) * p.H + h) * p.DV + j0 +
                                 kHalf * hf,
                             x);
+        }
+        arrive(B_ST + 8 * (c & 1));
         return true;
       };
       for (int c = 0; c < nck; ++c) {
-        const float a_next = load_a(c + 1);
+        // the last chunk's products end while this one's scores are computed
+        if (c > 0 && !(ok = out(c - 1))) break;
         if (!(ok = wait(B_DEC + 8 * (c & 1), c >> 1))) break;
         const float* sw = suff(c);
         const float* tot = tots(c);
-        const float pw = pref(c)[i];
+        const float a = decs(c)[i], pw = warp_prefix(a, lane);
         const float tot0 = tot[0], tot1 = tot[1], tot2 = tot[2];
         // the decays between block J and this row's
         float d0 = pw, d1 = pw;
@@ -247,9 +266,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         } else {
           d1 *= w4 == 2 ? tot1 : tot2;
         }
-        if (!(ok = wait(B_SC + 8 * (c & 1), c >> 1))) break;
+        if (!(ok = wait(B_SC, c))) break;
         tc_fence_after();
-        const uint32_t sc = row + TM_SC + 128 * (c & 1);
+        const uint32_t sc = row + TM_SC;
         uint32_t w0[16], w1[16];
         auto decay = [&](int J, float d, uint32_t* w) {
           float s[32];
@@ -294,11 +313,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         tmem_st_wait();
         tc_fence_before();
-        arrive(B_P + 8 * (c & 1));
+        arrive(B_P);
         arrive(B_DECE + 8 * (c & 1));
-        if (c > 0 && !(ok = out(c - 1))) break;
         pre = pw * (w4 > 0 ? tot0 : 1.f) * (w4 > 1 ? tot1 : 1.f) * (w4 > 2 ? tot2 : 1.f);
-        a = a_next;
       }
       if (ok && nck > 0) ok = out(nck - 1);
     }
@@ -352,19 +369,18 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         fence_proxy_async_smem();
       }
     };
-    operand();
-    arrive(B_SB);
-    float total = 1.f;
-    for (int c = 0; c < nck; ++c) {
+    float gamma = 1.f, total = 1.f;
+    // diag(suf) V of chunk c into its operand tiles
+    auto convert = [&](int c) -> bool {
       const int st = c & 1;
       const int len = len_of(c);
-      if (!(ok = wait(B_DEC + 8 * st, c >> 1))) break;
+      if (!wait(B_DEC + 8 * st, c >> 1)) return false;
       const float* tot = tots(c);
       float wgt = suff(c)[r];
       for (int bk = q4 + 1; bk < 4; ++bk) wgt *= tot[bk];
-      const float gamma = (tot[0] * tot[1]) * (tot[2] * tot[3]);
+      gamma = (tot[0] * tot[1]) * (tot[2] * tot[3]);
       arrive(B_DECE + 8 * st);
-      if (!(ok = wait(B_V + 8 * st, c >> 1) && (len == C || wait(B_K + 8 * st, c >> 1)))) break;
+      if (!wait(B_V + 8 * st, c >> 1) || (len < C && !wait(B_K + 8 * st, c >> 1))) return false;
       if (r < len) {
         uint4 raw[kHalf / 8];
 #pragma unroll
@@ -397,25 +413,39 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                                     sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
       }
       fence_proxy_async_smem();
+      tc_fence_before();
       arrive(B_VW);
+      return true;
+    };
+    if (nck > 0) {
+      operand();
+      arrive(B_SB);
+      ok = convert(0);
+    }
+    for (int c = 0; ok && c < nck; ++c) {
+      const int st = c & 1;
       if (!(ok = wait(B_D + 8 * st, c >> 1))) break;
       tc_fence_after();
-      {
 #pragma unroll
-        for (int e = 0; e < kHalf; e += 16) {
-          float x[16], y[16];
-          tmem_ld16(row + TM_D + kHalf * hf + e, x);
-          tmem_ld16(row + TM_D + BV + kHalf * hf + e, y);
-          tmem_ld_wait();
+      for (int e = 0; e < kHalf; e += 16) {
+        float x[16], y[16];
+        tmem_ld16(row + TM_D + kHalf * hf + e, x);
+        tmem_ld16(row + TM_D + BV + kHalf * hf + e, y);
+        tmem_ld_wait();
 #pragma unroll
-          for (int u = 0; u < 16; ++u) S[e + u] = fmaf(gamma, S[e + u], x[u] + y[u]);
-        }
+        for (int u = 0; u < 16; ++u) S[e + u] = fmaf(gamma, S[e + u], x[u] + y[u]);
       }
       total *= gamma;
-      if (!SUM && !(ok = wait(B_QS + 8 * st, c >> 1))) break;  // the old operand has been read
-      operand();
-      tc_fence_before();
-      arrive(B_SB);
+      if (c + 1 < nck) {
+        // the next product's operand first: it does not wait for the queries'
+        // product with this chunk's state
+        if (!(ok = convert(c + 1))) break;
+        if (!SUM) {
+          if (!(ok = wait(B_QS + 8 * st, c >> 1))) break;  // the old operand has been read
+          operand();
+          arrive(B_SB);
+        }
+      }
     }
     if (ok) {
       if (SUM) {
@@ -444,12 +474,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t ko = so + 1024 * (kk >> 2) + 2 * (kk & 3);
-          mma_f16(tmem + TM_SC + 128 * (c & 1), d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
+          mma_f16(tmem + TM_SC, d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
         }
-        mma_commit(bar + B_SC + 8 * (c & 1));
+        mma_commit(bar + B_SC);
       }
       __syncwarp();
-      mma_open = true; mma_off = B_SC + 8 * (c & 1); mma_par = c >> 1;
+      mma_open = true; mma_off = B_SC; mma_par = c;
     };
     if constexpr (!SUM) {
       if (nck > 0 && (ok = wait(B_Q, 0) && wait(B_K, 0))) scores(0);
@@ -457,21 +487,6 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     for (int c = 0; ok && c < nck; ++c) {
       const uint32_t st = c & 1;
       const uint64_t so = (uint64_t)st * (32768 >> 4);
-      // the state's operand is written, and the last product read
-      if (!(ok = wait(B_SB, c))) break;
-      if constexpr (!SUM) {
-        if (c > 0 && !(ok = wait(B_OE, c - 1))) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16(tmem + TM_O1, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
-                    id_qs, kk > 0 ? 1u : 0u);
-          mma_commit(bar + B_QS + 8 * st);
-        }
-        __syncwarp();
-        mma_open = true; mma_off = B_QS + 8 * st; mma_par = c >> 1;
-      }
       // (V's rows written implies V loaded; K is waited for in full here)
       if (!(ok = wait(B_VW, c) && wait(B_K + 8 * st, c >> 1))) break;
       tc_fence_after();
@@ -487,12 +502,25 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       mma_open = true; mma_off = B_D + 8 * st; mma_par = c >> 1;
       if constexpr (!SUM) {
-        if (!(ok = wait(B_P + 8 * st, c >> 1))) break;
+        if (!(ok = wait(B_SB, c) && (c < 2 || wait(B_OE + 8 * st, (c >> 1) - 1)))) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmem + TM_O2, tmem + TM_SC + 128 * st + 8 * kk, d_v + (so >> 1) + 128 * kk,
+            mma_f16(tmem + TM_O1 + 128 * st, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
+                    id_qs, kk > 0 ? 1u : 0u);
+          mma_commit(bar + B_QS + 8 * st);
+        }
+        __syncwarp();
+        mma_open = true; mma_off = B_QS + 8 * st; mma_par = c >> 1;
+      }
+      if constexpr (!SUM) {
+        if (!(ok = wait(B_P, c))) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ts(tmem + TM_O2 + 128 * st, tmem + TM_SC + 8 * kk, d_v + (so >> 1) + 128 * kk,
                        id_pv, kk > 0 ? 1u : 0u);
           mma_commit(bar + B_O + 8 * st);
         }
@@ -546,6 +574,16 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         tma_prefetch_2d(&tm_v, h * p.DV + j0, tok(c));
       };
+      // out of chunk c; on return its stage of V is free
+      auto send = [&](int c) -> bool {
+        if (!wait(B_ST + 8 * (c & 1), c >> 1)) return false;
+        if (staged(c)) {
+          tma_store_2d(&tm_o, sb + OFF_V + (c & 1) * 16384, h * p.DV + j0, tok(c));
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+        return true;
+      };
       int c = 0;
       for (; c < 2 && c < nck; ++c) {
         if (!SUM) load_q(c);
@@ -556,15 +594,19 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       prefetch(3);
       // chunk c takes the stage of chunk c - 2 as its parts become free
       for (; c < nck; ++c) {
+        if (!(ok = wait(B_D + 8 * (c & 1), (c >> 1) - 1))) break;
+        load_k(c);
         if constexpr (!SUM) {
           if (!(ok = wait(B_QS + 8 * (c & 1), (c >> 1) - 1))) break;
           load_q(c);
         }
-        if (!(ok = wait(B_D + 8 * (c & 1), (c >> 1) - 1))) break;
-        load_k(c);
-        if (!SUM && !(ok = wait(B_O + 8 * (c & 1), (c >> 1) - 1))) break;
+        if (!SUM && !(ok = send(c - 2))) break;
         load_v(c);
         prefetch(c + 2);
+      }
+      if constexpr (!SUM) {
+        for (int e = nck > 2 ? nck - 2 : 0; ok && e < nck; ++e) ok = send(e);
+        bulk_wait_all();
       }
       if (!ok) {
         // give the loads in flight their time before the block leaves
@@ -579,7 +621,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
       for (int bk = 0; bk < 4; ++bk) {
         const int t = 32 * bk + lane;
-        a[bk] = t < len ? p.al.at(tok0 + (int64_t)c * C + t, h) : 1.f;
+        a[bk] = t < len ? p.al.now(tok0 + (int64_t)c * C + t, h) : 1.f;
       }
     };
     float a[4], nx[4];
@@ -591,7 +633,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 #pragma unroll
       for (int bk = 0; bk < 4; ++bk) {
         const float pw = warp_prefix(a[bk], lane), sw = warp_suffix(a[bk], lane);
-        o[32 * bk + lane] = pw;
+        o[32 * bk + lane] = a[bk];
         o[128 + 32 * bk + lane] = sw;
         if (lane == 31) o[256 + bk] = pw;
         a[bk] = nx[bk];
@@ -642,9 +684,12 @@ cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const
   const bool varlen = cu != nullptr;
   const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
   CUtensorMap mq, mk, mv;
+  CUtensorMap mo = {};
   if (!bf16_map(&mq, q, (uint64_t)H * dk, rows, fw::C) ||
       !bf16_map(&mk, k, (uint64_t)H * dk, rows, fw::C) ||
       !bf16_map(&mv, v, (uint64_t)H * dv, rows, fw::C))
+    return cudaErrorInvalidValue;
+  if (out_dtype == CKDA_BF16 && !bf16_map(&mo, out, (uint64_t)H * dv, rows, fw::C))
     return cudaErrorInvalidValue;
   const int g = fwd_segments(n_seqs, T, H, dv, varlen);
   fw::Args a{{alpha, H, per_head}, S0, cu, out, S_final, n_seqs, T, H, dv, status, g, nullptr,
@@ -656,17 +701,17 @@ cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const
     a.dec = a.part + (size_t)n_seqs * H * g * dk * dv;
     auto ks = fw::la_fwd_kernel<float, true>;
     if ((e = max_smem<0>(ks, fw::kSmem)) != cudaSuccess) return e;
-    ks<<<units * (g - 1), fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, a);
+    ks<<<units * (g - 1), fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (out_dtype == CKDA_BF16) {
     auto kb = fw::la_fwd_kernel<__nv_bfloat16, false>;
     if ((e = max_smem<1>(kb, fw::kSmem)) != cudaSuccess) return e;
-    kb<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, a);
+    kb<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
   } else {
     auto kf = fw::la_fwd_kernel<float, false>;
     if ((e = max_smem<2>(kf, fw::kSmem)) != cudaSuccess) return e;
-    kf<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, a);
+    kf<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
   }
   return cudaGetLastError();
 }
