@@ -64,34 +64,34 @@ constexpr uint32_t OFF_SB = OFF_VW + 3 * 16384;  // bf16 state [128][64]
 constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x {a[128], sufW[128], tot[4]} fp32
 constexpr uint32_t kDecBytes = 1024 + 16;
 constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
-constexpr uint32_t OFF_MISC = OFF_BAR + 256;     // tensor-memory base, the sequence
+constexpr uint32_t OFF_MISC = OFF_BAR + 176;     // tensor-memory base, the sequence
 constexpr uint32_t kSmem = OFF_MISC + 16;
 static_assert(kSmem <= 232448, "shared memory");
 
 // mbarriers, byte offsets from OFF_BAR; each completes once per chunk (those
 // with two stages once per two)
 constexpr uint32_t B_Q = 0, B_K = 16, B_V = 32;  // stage loaded, + 8 (c & 1)
-constexpr uint32_t B_SC = 168;   // Q K^T complete (tensor core)
-constexpr uint32_t B_OE = 216;   // Q S and P V read, + 8 (c & 1)
-constexpr uint32_t B_ST = 232;   // out staged where V was (or stored), + 8 (c & 1)
-constexpr uint32_t B_PP = 184;   // scores read by both warps of 32 rows, + 8 (row block)
-constexpr uint32_t B_P = 48;     // P written
+constexpr uint32_t B_SC = 48;    // Q K^T complete (tensor core); the last chunk's P is free too
+constexpr uint32_t B_P = 56;     // P written, the scores read
 constexpr uint32_t B_VW = 64;    // diag(suf) V written, V's and K's tail rows cleared, the last
                                  // chunk's product read
 constexpr uint32_t B_SB = 72;    // the state's operand written
+constexpr uint32_t B_O = 80;     // Q S and P V complete (tensor core)
+constexpr uint32_t B_OE = 88;    // and read
 // complete (tensor core), + 8 (c & 1): the copy thread, which nothing holds
 // to the chunk, waits for these too
-constexpr uint32_t B_D = 88;     // K^T diag(suf) V
-constexpr uint32_t B_QS = 104;   // Q S
-constexpr uint32_t B_O = 120;    // Q S and P V
-constexpr uint32_t B_DEC = 136;  // decays of a chunk written, + 8 (c & 1)
-constexpr uint32_t B_DECE = 152; // and read, + 8 (c & 1)
+constexpr uint32_t B_D = 96;     // K^T diag(suf) V
+constexpr uint32_t B_QS = 112;   // Q S
+constexpr uint32_t B_ST = 128;   // out staged where V was (or stored), + 8 (c & 1)
+constexpr uint32_t B_DEC = 144;  // decays of a chunk written, + 8 (c & 1)
+constexpr uint32_t B_DECE = 160; // and read, + 8 (c & 1)
 
 // tensor-memory columns
-constexpr uint32_t TM_SC = 0;    // Q K^T; P (bf16 pairs) over its first 64
-constexpr uint32_t TM_O1 = 128;  // Q S, + 128 (c & 1)
-constexpr uint32_t TM_O2 = 192;  // P V, + 128 (c & 1)
-constexpr uint32_t TM_D = 384;   // K^T diag(suf) V: first term, second and third
+constexpr uint32_t TM_SC = 0;    // Q K^T
+constexpr uint32_t TM_P = 128;   // P, bf16 pairs
+constexpr uint32_t TM_O1 = 192;  // Q S
+constexpr uint32_t TM_O2 = 256;  // P V
+constexpr uint32_t TM_D = 320;   // K^T diag(suf) V: first term, second and third
 constexpr uint32_t kTmemCols = 512;
 
 constexpr int kThreads = 608;
@@ -145,18 +145,16 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
 
   const uint32_t bar = sb + OFF_BAR;
   if (tid == 0) {
-    for (int i = 0; i < 6; ++i) mbar_init(bar + 8 * i, 1);
+    for (int i = 0; i < 7; ++i) mbar_init(bar + 8 * i, 1);  // Q, K, V, scores
+    mbar_init(bar + B_P, 8);
     mbar_init(bar + B_VW, 8);
     mbar_init(bar + B_SB, 8);
-    mbar_init(bar + B_SC, 1);
-    mbar_init(bar + B_P, 8);
-    for (int i = 0; i < 4; ++i) mbar_init(bar + B_PP + 8 * i, 2);
+    mbar_init(bar + B_O, 1);
+    mbar_init(bar + B_OE, 8);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar + B_OE + 8 * i, 8);
-      mbar_init(bar + B_ST + 8 * i, 8);
       mbar_init(bar + B_D + 8 * i, 1);
       mbar_init(bar + B_QS + 8 * i, 1);
-      mbar_init(bar + B_O + 8 * i, 1);
+      mbar_init(bar + B_ST + 8 * i, 8);
       mbar_init(bar + B_DEC + 8 * i, 1);
       mbar_init(bar + B_DECE + 8 * i, SUM ? 8 : 16);
     }
@@ -184,7 +182,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     return left < C ? (int)left : C;
   };
   auto wait = [&](uint32_t off, uint32_t par) -> bool {
-    return mbar_wait_bounded(bar + off, par & 1u, kWaitNs);
+    return mbar_wait_small(bar + off, par & 1u, kWaitNs);
   };
   const float* dec0 = reinterpret_cast<const float*>(sm + OFF_DEC);
   auto decs = [&](int c) { return dec0 + (c & 1) * (kDecBytes / 4); };
@@ -206,118 +204,113 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   bool mma_open = false;
   uint32_t mma_off = 0, mma_par = 0;
 
+  // Loops whose code would not stay in the instruction cache when unrolled
+  // (19 warps run five different programs) are kept rolled on purpose.
   if (warp < 8) {
     // ---- scores and out ---------------------------------------------------------------------
     if constexpr (!SUM) {
       const int w4 = warp & 3, hf = warp >> 2;  // row block; which of its two warps
       const int i = 32 * w4 + lane;             // row
       const uint32_t row = tmem + ((uint32_t)(32 * w4) << 16);
-      // 32-column blocks of the scores: the first warp takes the diagonal one
-      // (and, of the last rows, block 0), the second those left of it
-      const bool has0 = hf == 0 || w4 >= 1, has1 = hf == 0 ? w4 == 3 : w4 >= 2;
-      const int J0 = hf == 0 ? w4 : w4 - 1, J1 = hf == 0 ? 0 : w4 - 2;
+      if (hf == 0) {
+        // blocks right of the diagonal stay zero
+        uint32_t z[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z[e] = 0u;
+#pragma unroll 1
+        for (int J = w4 + 1; J < 4; ++J) tmem_st16(row + TM_P + 16 * J, z);
+        tmem_st_wait();
+      }
       float pre = 0.f;
-      auto out = [&](int c) -> bool {
-        if (!wait(B_O + 8 * (c & 1), c >> 1)) return false;
-        tc_fence_after();
-        float x[kHalf];
-        tmem_ld32(row + TM_O2 + 128 * (c & 1) + kHalf * hf, x);
+#pragma unroll 1
+      for (int c = 0; c <= nck; ++c) {
+        if (c > 0) {
+          // out of the last chunk: its products end while this one's scores
+          // are computed
+          const int e = c - 1;
+          if (!(ok = wait(B_O, e))) break;
+          tc_fence_after();
+          const bool st = staged(e), in = i < len_of(e);
+          Tout* o = static_cast<Tout*>(p.out) +
+                    ((size_t)(tok0 + (int64_t)e * C + i) * p.H + h) * p.DV + j0 + kHalf * hf;
+#pragma unroll 1
+          for (int u0 = 0; u0 < kHalf; u0 += 16) {
+            float x[16], y[16];
+            tmem_ld16(row + TM_O1 + kHalf * hf + u0, y);
+            tmem_ld16(row + TM_O2 + kHalf * hf + u0, x);
+            tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < kHalf; e += 16) {
-          float y[16];
-          tmem_ld16(row + TM_O1 + 128 * (c & 1) + kHalf * hf + e, y);
-          tmem_ld_wait();
+            for (int u = 0; u < 16; ++u) x[u] = fmaf(pre, y[u], x[u]);
+            if (st) {
 #pragma unroll
-          for (int u = 0; u < 16; ++u) x[e + u] = fmaf(pre, y[u], x[e + u]);
-        }
-        tc_fence_before();
-        arrive(B_OE + 8 * (c & 1));
-        if (staged(c)) {
-#pragma unroll
-          for (int c8 = 0; c8 < kHalf / 8; ++c8) {
-            const float* y = x + 8 * c8;
-            *reinterpret_cast<uint4*>(sm + OFF_V + (c & 1) * 16384 +
-                                      sw128_chunk(i, kHalf * hf + 8 * c8, 128)) =
-                make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                           pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+              for (int c8 = 0; c8 < 2; ++c8)
+                *reinterpret_cast<uint4*>(sm + OFF_V + (e & 1) * 16384 +
+                                          sw128_chunk(i, kHalf * hf + u0 + 8 * c8, 128)) =
+                    pack8(x + 8 * c8);
+            } else if (in) {
+              store_cols<16>(o + u0, x);
+            }
           }
+          tc_fence_before();
           fence_proxy_async_smem();
-        } else if (i < len_of(c)) {
-          store_cols<kHalf>(static_cast<Tout*>(p.out) +
-                                ((size_t)(tok0 + (int64_t)c * C + i) * p.H + h) * p.DV + j0 +
-                                kHalf * hf,
-                            x);
+          arrive(B_OE);
+          if (lane == 0) mbar_arrive(bar + B_ST + 8 * (e & 1));
         }
-        arrive(B_ST + 8 * (c & 1));
-        return true;
-      };
-      for (int c = 0; c < nck; ++c) {
-        // the last chunk's products end while this one's scores are computed
-        if (c > 0 && !(ok = out(c - 1))) break;
+        if (c == nck) break;
         if (!(ok = wait(B_DEC + 8 * (c & 1), c >> 1))) break;
         const float* sw = suff(c);
-        const float* tot = tots(c);
+        const float4 tot = *reinterpret_cast<const float4*>(tots(c));
         const float a = decs(c)[i], pw = warp_prefix(a, lane);
-        const float tot0 = tot[0], tot1 = tot[1], tot2 = tot[2];
-        // the decays between block J and this row's
-        float d0 = pw, d1 = pw;
-        if (hf == 0) {
-          if (w4 == 3) d1 *= tot1 * tot2;
-        } else {
-          d1 *= w4 == 2 ? tot1 : tot2;
-        }
         if (!(ok = wait(B_SC, c))) break;
         tc_fence_after();
-        const uint32_t sc = row + TM_SC;
-        uint32_t w0[16], w1[16];
-        auto decay = [&](int J, float d, uint32_t* w) {
-          float s[32];
-          tmem_ld32(sc + 32 * J, s);
-          tmem_ld_wait();
-          const float* x = sw + 32 * J;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 f = *reinterpret_cast<const float4*>(x + 4 * e);
-            w[2 * e] = pack_bf16x2(s[4 * e] * (d * f.x), s[4 * e + 1] * (d * f.y));
-            w[2 * e + 1] = pack_bf16x2(s[4 * e + 2] * (d * f.z), s[4 * e + 3] * (d * f.w));
-          }
-        };
+        float s[32];
+        uint32_t w[16];
         if (hf == 0) {
           // the diagonal block: D(i, j) runs down from 1 at j = i
-          float s0[32], run = 1.f;
-          tmem_ld32(sc + 32 * J0, s0);
+          tmem_ld32(row + TM_SC + 32 * w4, s);
           tmem_ld_wait();
+          float run = 1.f;
 #pragma unroll
           for (int j = 31; j >= 0; --j) {
             const float aj = __shfl_sync(0xffffffffu, a, j);
-            s0[j] = j <= lane ? s0[j] * run : 0.f;
+            s[j] = j <= lane ? s[j] * run : 0.f;
             run = j <= lane ? run * aj : run;
           }
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w0[e] = pack_bf16x2(s0[2 * e], s0[2 * e + 1]);
-        } else if (has0) {
-          decay(J0, d0, w0);
+          for (int e = 0; e < 16; ++e) w[e] = pack_bf16x2(s[2 * e], s[2 * e + 1]);
+          tmem_st16(row + TM_P + 16 * w4, w);
         }
-        if (has1) decay(J1, d1, w1);
-        tc_fence_before();
-        arrive(B_PP + 8 * w4);
-        // P lies over scores that the other warp reads
-        if (!(ok = wait(B_PP + 8 * w4, c))) break;
-        tc_fence_after();
-        if (has0) tmem_st16(sc + 16 * J0, w0);
-        if (has1) tmem_st16(sc + 16 * J1, w1);
-        if (hf == 1) {
+        // blocks left of it: of the last rows the first warp takes block 0,
+        // the second warp takes the others
+        const int Jlo = hf == 0 ? 0 : (w4 == 3 ? 1 : 0);
+        const int Jhi = hf == 0 ? (w4 == 3 ? 0 : -1) : w4 - 1;
+#pragma unroll 1
+        for (int J = Jhi; J >= Jlo; --J) {
+          tmem_ld32(row + TM_SC + 32 * J, s);
+          // the decays between block J and this row's
+          float d = pw;
+          if (w4 > 1 && J < 1) d *= tot.y;
+          if (w4 > 2 && J < 2) d *= tot.z;
+          const float2 d2 = make_float2(d, d);
+          tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) w0[e] = 0u;
-          for (int J = w4 + 1; J < 4; ++J) tmem_st16(sc + 16 * J, w0);
+          for (int e = 0; e < 8; ++e) {
+            const float4 f = *reinterpret_cast<const float4*>(sw + 32 * J + 4 * e);
+            const float2 x = mul2(make_float2(s[4 * e], s[4 * e + 1]),
+                                  mul2(d2, make_float2(f.x, f.y)));
+            const float2 y = mul2(make_float2(s[4 * e + 2], s[4 * e + 3]),
+                                  mul2(d2, make_float2(f.z, f.w)));
+            w[2 * e] = pack_bf16x2(x.x, x.y);
+            w[2 * e + 1] = pack_bf16x2(y.x, y.y);
+          }
+          tmem_st16(row + TM_P + 16 * J, w);
         }
         tmem_st_wait();
         tc_fence_before();
         arrive(B_P);
-        arrive(B_DECE + 8 * (c & 1));
-        pre = pw * (w4 > 0 ? tot0 : 1.f) * (w4 > 1 ? tot1 : 1.f) * (w4 > 2 ? tot2 : 1.f);
+        if (lane == 0) mbar_arrive(bar + B_DECE + 8 * (c & 1));
+        pre = pw * (w4 > 0 ? tot.x : 1.f) * (w4 > 1 ? tot.y : 1.f) * (w4 > 2 ? tot.z : 1.f);
       }
-      if (ok && nck > 0) ok = out(nck - 1);
     }
   } else if (warp < 16) {
     // ---- state ----------------------------------------------------------------------------
@@ -330,126 +323,126 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const size_t unit = (size_t)n * p.H + h;
     const size_t at = ((size_t)r * p.DV) + j0 + kHalf * hf;  // this thread's columns of a state
     const size_t stsz = (size_t)DK * p.DV;
-    auto add = [&](const float* src, float f) {
-#pragma unroll
-      for (int e = 0; e < kHalf; e += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src + e);
-        S[e] = fmaf(f, x.x, S[e]);
-        S[e + 1] = fmaf(f, x.y, S[e + 1]);
-        S[e + 2] = fmaf(f, x.z, S[e + 2]);
-        S[e + 3] = fmaf(f, x.w, S[e + 3]);
-      }
-    };
-    if (seg == 0) {
-      // (with segments the last one may write S_final over S0 before this
-      // block starts: the first launch keeps a copy)
-      if (p.S0 != nullptr) {
-        if (!SUM && p.seg_n > 1)
-          add(p.part + unit * p.seg_n * stsz + at, 1.f);
-        else
-          add(p.S0 + unit * stsz + at, 1.f);
-      }
-      if (SUM && p.S0 != nullptr) store_cols<kHalf>(p.part + unit * p.seg_n * stsz + at, S);
-    } else if (!SUM) {
+    float* part = p.part + unit * p.seg_n * stsz + at;
+    {
+      // segment 0 starts from S0; with segments, from a copy of it that the
+      // first launch keeps (the last segment may write S_final over S0 before
+      // this block starts); segment g from the decayed sum of the end states
+      // before it
       float f = 1.f;
-      for (int g = seg; g >= 1; --g) {
-        add(p.part + (unit * p.seg_n + g) * stsz + at, f);
-        f *= p.dec[unit * p.seg_n + g - 1];
-      }
-    }
-    auto operand = [&]() {
-      if constexpr (!SUM) {
+#pragma unroll 1
+      for (int g = seg; g >= 0; --g) {
+        const float* src = nullptr;
+        if (g > 0)
+          src = SUM ? nullptr : part + g * stsz;
+        else if (seg == 0 && p.S0 != nullptr)
+          src = !SUM && p.seg_n > 1 ? part : p.S0 + unit * stsz + at;
+        if (src != nullptr) {
 #pragma unroll
-        for (int c8 = 0; c8 < kHalf / 8; ++c8) {
-          const float* x = S + 8 * c8;
-          *reinterpret_cast<uint4*>(sm + OFF_SB + sw128_chunk(r, kHalf * hf + 8 * c8, 128)) =
-              make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                         pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          for (int e = 0; e < kHalf; e += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(src + e);
+            S[e] = fmaf(f, x.x, S[e]);
+            S[e + 1] = fmaf(f, x.y, S[e + 1]);
+            S[e + 2] = fmaf(f, x.z, S[e + 2]);
+            S[e + 3] = fmaf(f, x.w, S[e + 3]);
+          }
         }
-        fence_proxy_async_smem();
+        if (!SUM && g > 0) f *= p.dec[unit * p.seg_n + g - 1];
       }
-    };
+      if (SUM && seg == 0 && p.S0 != nullptr) store_cols<kHalf>(part, S);
+    }
     float gamma = 1.f, total = 1.f;
-    // diag(suf) V of chunk c into its operand tiles
-    auto convert = [&](int c) -> bool {
+#pragma unroll 1
+    for (int c = 0; c <= nck; ++c) {
+      if (c > 0) {
+        if (!(ok = wait(B_D + 8 * ((c - 1) & 1), (c - 1) >> 1))) break;
+        tc_fence_after();
+        const float2 g2 = make_float2(gamma, gamma);
+#pragma unroll
+        for (int e = 0; e < kHalf; e += 16) {
+          float x[16], y[16];
+          tmem_ld16(row + TM_D + kHalf * hf + e, x);
+          tmem_ld16(row + TM_D + BV + kHalf * hf + e, y);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 16; u += 2) {
+            const float2 d = add2(make_float2(x[u], x[u + 1]), make_float2(y[u], y[u + 1]));
+            const float2 z = fma2(g2, make_float2(S[e + u], S[e + u + 1]), d);
+            S[e + u] = z.x;
+            S[e + u + 1] = z.y;
+          }
+        }
+        total *= gamma;
+      }
+      if (c == nck) break;
+      // diag(suf) V into the product's operand, before the state's: it does
+      // not wait for the queries' product with the last chunk's state
       const int st = c & 1;
       const int len = len_of(c);
-      if (!wait(B_DEC + 8 * st, c >> 1)) return false;
-      const float* tot = tots(c);
-      float wgt = suff(c)[r];
-      for (int bk = q4 + 1; bk < 4; ++bk) wgt *= tot[bk];
-      gamma = (tot[0] * tot[1]) * (tot[2] * tot[3]);
-      arrive(B_DECE + 8 * st);
-      if (!wait(B_V + 8 * st, c >> 1) || (len < C && !wait(B_K + 8 * st, c >> 1))) return false;
-      if (r < len) {
-        uint4 raw[kHalf / 8];
+      if (!(ok = wait(B_DEC + 8 * st, c >> 1))) break;
+      {
+        const float4 tot = *reinterpret_cast<const float4*>(tots(c));
+        const float wgt = suff(c)[r] * (q4 < 1 ? tot.y : 1.f) * (q4 < 2 ? tot.z : 1.f) *
+                          (q4 < 3 ? tot.w : 1.f);
+        gamma = (tot.x * tot.y) * (tot.z * tot.w);
+        arrive(B_DECE + 8 * st);
+        if (!(ok = wait(B_V + 8 * st, c >> 1))) break;
+        if (len < C && !(ok = wait(B_K + 8 * st, c >> 1))) break;
+        if (r < len) {
+          const float2 w2 = make_float2(wgt, wgt);
+#pragma unroll 1
+          for (int h2 = 0; h2 < 2; ++h2) {
+            const uint32_t o0 = sw128_chunk(r, kHalf * hf + 16 * h2, 128);
+            const uint32_t o1 = o0 ^ 16u;  // the next 16 bytes under the swizzle
+            const uint4 ra = *reinterpret_cast<const uint4*>(sm + OFF_V + st * 16384 + o0);
+            const uint4 rb = *reinterpret_cast<const uint4*>(sm + OFF_V + st * 16384 + o1);
+            const uint32_t in[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+            uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
-        for (int c8 = 0; c8 < kHalf / 8; ++c8)
-          raw[c8] = *reinterpret_cast<const uint4*>(sm + OFF_V + st * 16384 +
-                                                    sw128_chunk(r, kHalf * hf + 8 * c8, 128));
+            for (int e = 0; e < 8; ++e) split3(in[e], w2, &t1[e], &t2[e], &t3[e]);
+            uint8_t* d = sm + OFF_VW;
+            *reinterpret_cast<uint4*>(d + o0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+            *reinterpret_cast<uint4*>(d + o1) = make_uint4(t1[4], t1[5], t1[6], t1[7]);
+            *reinterpret_cast<uint4*>(d + 16384 + o0) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+            *reinterpret_cast<uint4*>(d + 16384 + o1) = make_uint4(t2[4], t2[5], t2[6], t2[7]);
+            *reinterpret_cast<uint4*>(d + 32768 + o0) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+            *reinterpret_cast<uint4*>(d + 32768 + o1) = make_uint4(t3[4], t3[5], t3[6], t3[7]);
+          }
+        } else {
+          // past the sequence's end lie other tokens, or none: V and K rows
+          // cleared, so that no product meets what is not finite there
+          const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+          for (int c8 = 0; c8 < kHalf / 8; ++c8) {
+            const uint32_t o = sw128_chunk(r, kHalf * hf + 8 * c8, 128);
+            *reinterpret_cast<uint4*>(sm + OFF_V + st * 16384 + o) = z;
 #pragma unroll
-        for (int c8 = 0; c8 < kHalf / 8; ++c8) {
-          const uint32_t in[4] = {raw[c8].x, raw[c8].y, raw[c8].z, raw[c8].w};
-          uint32_t t1[4], t2[4], t3[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) split3(in[e], wgt, &t1[e], &t2[e], &t3[e]);
-          uint8_t* d = sm + OFF_VW + sw128_chunk(r, kHalf * hf + 8 * c8, 128);
-          *reinterpret_cast<uint4*>(d) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-          *reinterpret_cast<uint4*>(d + 16384) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-          *reinterpret_cast<uint4*>(d + 32768) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+            for (int e = 0; e < 3; ++e)
+              *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 + o) = z;
+          }
+#pragma unroll 1
+          for (int c8 = 0; c8 < DK / 16; ++c8)
+            *reinterpret_cast<uint4*>(sm + OFF_K + st * 32768 +
+                                      sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
         }
-      } else {
-        // past the sequence's end lie other tokens, or none: V and K rows
-        // cleared, so that no product meets what is not finite there
-        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-        for (int c8 = 0; c8 < kHalf / 8; ++c8) {
-          const uint32_t o = sw128_chunk(r, kHalf * hf + 8 * c8, 128);
-          *reinterpret_cast<uint4*>(sm + OFF_V + st * 16384 + o) = z;
-          for (int e = 0; e < 3; ++e)
-            *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 + o) = z;
-        }
-        for (int c8 = 0; c8 < DK / 16; ++c8)
-          *reinterpret_cast<uint4*>(sm + OFF_K + st * 32768 +
-                                    sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
       }
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(B_VW);
-      return true;
-    };
-    if (nck > 0) {
-      operand();
-      arrive(B_SB);
-      ok = convert(0);
-    }
-    for (int c = 0; ok && c < nck; ++c) {
-      const int st = c & 1;
-      if (!(ok = wait(B_D + 8 * st, c >> 1))) break;
-      tc_fence_after();
+      if constexpr (!SUM) {
+        // (the old operand has been read)
+        if (c > 0 && !(ok = wait(B_QS + 8 * (st ^ 1), (c - 1) >> 1))) break;
 #pragma unroll
-      for (int e = 0; e < kHalf; e += 16) {
-        float x[16], y[16];
-        tmem_ld16(row + TM_D + kHalf * hf + e, x);
-        tmem_ld16(row + TM_D + BV + kHalf * hf + e, y);
-        tmem_ld_wait();
-#pragma unroll
-        for (int u = 0; u < 16; ++u) S[e + u] = fmaf(gamma, S[e + u], x[u] + y[u]);
-      }
-      total *= gamma;
-      if (c + 1 < nck) {
-        // the next product's operand first: it does not wait for the queries'
-        // product with this chunk's state
-        if (!(ok = convert(c + 1))) break;
-        if (!SUM) {
-          if (!(ok = wait(B_QS + 8 * st, c >> 1))) break;  // the old operand has been read
-          operand();
-          arrive(B_SB);
-        }
+        for (int c8 = 0; c8 < kHalf / 8; ++c8)
+          *reinterpret_cast<uint4*>(sm + OFF_SB + sw128_chunk(r, kHalf * hf + 8 * c8, 128)) =
+              pack8(S + 8 * c8);
+        fence_proxy_async_smem();
+        arrive(B_SB);
       }
     }
     if (ok) {
       if (SUM) {
-        store_cols<kHalf>(p.part + (unit * p.seg_n + seg + 1) * stsz + at, S);
+        store_cols<kHalf>(part + (seg + 1) * stsz, S);
         if (r == 0 && hf == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = total;
       } else if (p.Sf != nullptr && seg == p.seg_n - 1) {
         store_cols<kHalf>(p.Sf + unit * stsz + at, S);
@@ -471,7 +464,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     auto scores = [&](int c) {
       const uint64_t so = (uint64_t)(c & 1) * (32768 >> 4);
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t ko = so + 1024 * (kk >> 2) + 2 * (kk & 3);
           mma_f16(tmem + TM_SC, d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
@@ -491,10 +484,10 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (!(ok = wait(B_VW, c) && wait(B_K + 8 * st, c >> 1))) break;
       tc_fence_after();
       if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
         for (int kk = 0; kk < 8; ++kk)
           mma_f16(tmem + TM_D, d_km + so + 128 * kk, d_vw + 128 * kk, id_kv2, kk > 0 ? 1u : 0u);
-#pragma unroll
+#pragma unroll 2
         for (int kk = 0; kk < 8; ++kk)
           mma_f16(tmem + TM_D + BV, d_km + so + 128 * kk, d_vw + (32768 >> 4) + 128 * kk, id_kv1, 1u);
         mma_commit(bar + B_D + 8 * st);
@@ -502,12 +495,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       mma_open = true; mma_off = B_D + 8 * st; mma_par = c >> 1;
       if constexpr (!SUM) {
-        if (!(ok = wait(B_SB, c) && (c < 2 || wait(B_OE + 8 * st, (c >> 1) - 1)))) break;
+        if (!(ok = wait(B_SB, c) && (c == 0 || wait(B_OE, c - 1)))) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16(tmem + TM_O1 + 128 * st, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
+            mma_f16(tmem + TM_O1, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
                     id_qs, kk > 0 ? 1u : 0u);
           mma_commit(bar + B_QS + 8 * st);
         }
@@ -518,14 +511,14 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!(ok = wait(B_P, c))) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll
+#pragma unroll 2
           for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ts(tmem + TM_O2 + 128 * st, tmem + TM_SC + 8 * kk, d_v + (so >> 1) + 128 * kk,
+            mma_f16_ts(tmem + TM_O2, tmem + TM_P + 8 * kk, d_v + (so >> 1) + 128 * kk,
                        id_pv, kk > 0 ? 1u : 0u);
-          mma_commit(bar + B_O + 8 * st);
+          mma_commit(bar + B_O);
         }
         __syncwarp();
-        mma_off = B_O + 8 * st;
+        mma_off = B_O; mma_par = c;
         // the next chunk's scores, last: K comes into its stage only after
         // the last chunk's product with it, and is then still on its way
         if (c + 1 < nck) {

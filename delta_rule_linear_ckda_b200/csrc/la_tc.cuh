@@ -55,31 +55,27 @@ __device__ __forceinline__ float warp_suffix(float a, int lane) {
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
 __device__ __forceinline__ float hi_f(uint32_t x) { return __uint_as_float(x & 0xffff0000u); }
 
-// A pair of fp32 values as the sum of three bf16 values each: 24 bits.
-__device__ __forceinline__ void split3f(float a, float b, uint32_t* t1, uint32_t* t2,
-                                        uint32_t* t3) {
-  *t1 = sm100::pack_bf16x2(a, b);
-  a -= lo_f(*t1);
-  b -= hi_f(*t1);
-  *t2 = sm100::pack_bf16x2(a, b);
-  a -= lo_f(*t2);
-  b -= hi_f(*t2);
-  *t3 = sm100::pack_bf16x2(a, b);
+// A pair of bf16 values times w as the sum of three bf16 pairs: 24 bits.
+__device__ __forceinline__ void split3(uint32_t in, float2 w, uint32_t* t1, uint32_t* t2,
+                                       uint32_t* t3) {
+  const float2 m1 = make_float2(-1.f, -1.f);
+  float2 x = mul2(make_float2(lo_f(in), hi_f(in)), w);
+  *t1 = sm100::pack_bf16x2(x.x, x.y);
+  x = fma2(make_float2(lo_f(*t1), hi_f(*t1)), m1, x);
+  *t2 = sm100::pack_bf16x2(x.x, x.y);
+  x = fma2(make_float2(lo_f(*t2), hi_f(*t2)), m1, x);
+  *t3 = sm100::pack_bf16x2(x.x, x.y);
 }
 
-// A pair of bf16 values times w, split.
-__device__ __forceinline__ void split3(uint32_t in, float w, uint32_t* t1, uint32_t* t2,
-                                       uint32_t* t3) {
-  split3f(lo_f(in) * w, hi_f(in) * w, t1, t2, t3);
+__device__ __forceinline__ uint4 pack8(const float* x) {
+  return make_uint4(sm100::pack_bf16x2(x[0], x[1]), sm100::pack_bf16x2(x[2], x[3]),
+                    sm100::pack_bf16x2(x[4], x[5]), sm100::pack_bf16x2(x[6], x[7]));
 }
 
 template <int N>
 __device__ __forceinline__ void store_cols(__nv_bfloat16* o, const float* x) {
 #pragma unroll
-  for (int e = 0; e < N; e += 8)
-    *reinterpret_cast<uint4*>(o + e) = make_uint4(
-        sm100::pack_bf16x2(x[e], x[e + 1]), sm100::pack_bf16x2(x[e + 2], x[e + 3]),
-        sm100::pack_bf16x2(x[e + 4], x[e + 5]), sm100::pack_bf16x2(x[e + 6], x[e + 7]));
+  for (int e = 0; e < N; e += 8) *reinterpret_cast<uint4*>(o + e) = pack8(x + e);
 }
 
 template <int N>

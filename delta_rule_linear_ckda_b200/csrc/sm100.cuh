@@ -93,6 +93,30 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
   }
 }
 
+// The same in a few instructions, for kernels whose many waits would crowd
+// the instruction cache.
+__device__ __forceinline__ bool mbar_wait_small(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u64 t, e;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 e, %%globaltimer;\n\t"
+      "add.u64 e, e, %3;\n"
+      "AGAIN:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "@p bra DONE;\n\t"
+      "mov.u64 t, %%globaltimer;\n\t"
+      "setp.lt.u64 q, t, e;\n\t"
+      "@q bra AGAIN;\n"
+      "DONE:\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "l"(limit_ns)
+      : "memory");
+  return ok != 0;
+}
+
 // One lane of a converged warp (the same one every time).  A branch on this
 // keeps the operands of what it guards in uniform registers; behind a branch
 // on the lane index the compiler moves each of them there by itself, about
