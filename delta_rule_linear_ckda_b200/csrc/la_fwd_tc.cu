@@ -31,9 +31,9 @@
 // Roundings: the scores (after their decays) and the state's copy that the
 // queries read are rounded once to bf16, like the inputs; both only reach
 // out.  The state itself stays at fp32 accuracy: diag(suf) V is split into
-// three bf16 terms (24 bits) whose products with the exact bf16 K are summed:
-// two terms side by side in one MMA (N = 128), which reads K from shared
-// memory once for both, and the third on top of the second.
+// three bf16 terms (24 bits) whose products with the exact bf16 K are one MMA
+// with the terms side by side (N = 192): shared memory, whose bandwidth bounds
+// this kernel, is read for K once instead of three times.
 //
 // A sequence may be split into segments that run at the same time (few
 // sequences and heads): a first launch computes each segment's own end state
@@ -91,7 +91,7 @@ constexpr uint32_t TM_SC = 0;    // Q K^T
 constexpr uint32_t TM_P = 128;   // P, bf16 pairs
 constexpr uint32_t TM_O1 = 192;  // Q S
 constexpr uint32_t TM_O2 = 256;  // P V
-constexpr uint32_t TM_D = 320;   // K^T diag(suf) V: first term, second and third
+constexpr uint32_t TM_D = 320;   // K^T diag(suf) V, three terms
 constexpr uint32_t kTmemCols = 512;
 
 constexpr int kThreads = 608;
@@ -121,7 +121,8 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               const __grid_constant__ CUtensorMap tm_o, const Args p) {
   extern __shared__ __align__(1024) uint8_t sm[];
   const uint32_t sb = smem_u32(sm);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // (through a shuffle, so that the compiler knows the warp index as uniform)
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
 
   // (the swizzled tiles need this; the base of dynamic shared memory has it)
   if ((sb & 1023u) != 0) {
@@ -171,11 +172,13 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC);
+  const uint32_t tmem =
+      __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC), 0);
 
   const int nck_all = (int)((sr.end - sr.begin + C - 1) / C);
   const int cbeg = (int)((int64_t)seg * nck_all / p.seg_n);
-  const int nck = (int)((int64_t)(seg + 1) * nck_all / p.seg_n) - cbeg;
+  const int nck =
+      __shfl_sync(0xffffffffu, (int)((int64_t)(seg + 1) * nck_all / p.seg_n) - cbeg, 0);
   const int64_t tok0 = sr.begin + (int64_t)cbeg * C;
   auto len_of = [&](int c) -> int {
     const int64_t left = sr.end - (tok0 + (int64_t)c * C);
@@ -360,13 +363,15 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const float2 g2 = make_float2(gamma, gamma);
 #pragma unroll
         for (int e = 0; e < kHalf; e += 16) {
-          float x[16], y[16];
+          float x[16], y[16], z3[16];
           tmem_ld16(row + TM_D + kHalf * hf + e, x);
           tmem_ld16(row + TM_D + BV + kHalf * hf + e, y);
+          tmem_ld16(row + TM_D + 2 * BV + kHalf * hf + e, z3);
           tmem_ld_wait();
 #pragma unroll
           for (int u = 0; u < 16; u += 2) {
-            const float2 d = add2(make_float2(x[u], x[u + 1]), make_float2(y[u], y[u + 1]));
+            const float2 d = add2(make_float2(x[u], x[u + 1]),
+                                  add2(make_float2(y[u], y[u + 1]), make_float2(z3[u], z3[u + 1])));
             const float2 z = fma2(g2, make_float2(S[e + u], S[e + u + 1]), d);
             S[e + u] = z.x;
             S[e + u + 1] = z.y;
@@ -460,11 +465,11 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     constexpr uint32_t id_sc = idesc_bf16(128, 128, 0, 0);
     constexpr uint32_t id_qs = idesc_bf16(128, BV, 0, 1);
     constexpr uint32_t id_pv = idesc_bf16(128, BV, 0, 1);
-    constexpr uint32_t id_kv2 = idesc_bf16(128, 2 * BV, 1, 1), id_kv1 = idesc_bf16(128, BV, 1, 1);
+    constexpr uint32_t id_kv = idesc_bf16(128, 3 * BV, 1, 1);
     auto scores = [&](int c) {
       const uint64_t so = (uint64_t)(c & 1) * (32768 >> 4);
       if (elect_one()) {
-#pragma unroll 2
+#pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
           const uint64_t ko = so + 1024 * (kk >> 2) + 2 * (kk & 3);
           mma_f16(tmem + TM_SC, d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
@@ -484,12 +489,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (!(ok = wait(B_VW, c) && wait(B_K + 8 * st, c >> 1))) break;
       tc_fence_after();
       if (elect_one()) {
-#pragma unroll 2
+#pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          mma_f16(tmem + TM_D, d_km + so + 128 * kk, d_vw + 128 * kk, id_kv2, kk > 0 ? 1u : 0u);
-#pragma unroll 2
-        for (int kk = 0; kk < 8; ++kk)
-          mma_f16(tmem + TM_D + BV, d_km + so + 128 * kk, d_vw + (32768 >> 4) + 128 * kk, id_kv1, 1u);
+          mma_f16(tmem + TM_D, d_km + so + 128 * kk, d_vw + 128 * kk, id_kv, kk > 0 ? 1u : 0u);
         mma_commit(bar + B_D + 8 * st);
       }
       __syncwarp();
@@ -498,7 +500,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!(ok = wait(B_SB, c) && (c == 0 || wait(B_OE, c - 1)))) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll 2
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_f16(tmem + TM_O1, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
                     id_qs, kk > 0 ? 1u : 0u);
@@ -511,7 +513,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         if (!(ok = wait(B_P, c))) break;
         tc_fence_after();
         if (elect_one()) {
-#pragma unroll 2
+#pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_f16_ts(tmem + TM_O2, tmem + TM_P + 8 * kk, d_v + (so >> 1) + 128 * kk,
                        id_pv, kk > 0 ? 1u : 0u);
