@@ -30,6 +30,14 @@ cudaError_t launch_la_bwd_simt(int dtype, int dk_, int dv_, const void* q, const
                                const int32_t* cu, const void* dO, const float* dSf, void* dq,
                                void* dk, void* dv, float* dalpha, float* dS0, void* ws, int n_seqs,
                                int T, int H, int* status, cudaStream_t stream);
+bool la_bwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen);
+size_t la_bwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen,
+                                 bool per_head);
+cudaError_t launch_la_bwd_tc(int dk_, int dv_, const void* q, const void* k, const void* v,
+                             const float* alpha, int per_head, const float* S0, const int32_t* cu,
+                             const void* dO, const float* dSf, void* dq, void* dk, void* dv,
+                             float* dalpha, float* dS0, void* ws, int n_seqs, int T, int H,
+                             int* status, cudaStream_t stream);
 cudaError_t launch_qk_norm_fwd(const qkn::Args& p, int dtype, int out_dtype, cudaStream_t st);
 cudaError_t launch_qk_norm_bwd(const qkn::Args& p, int dtype, float* dwq, float* dwk,
                                cudaStream_t st);
@@ -153,8 +161,10 @@ int64_t ckda_la_bwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int a
   const int rc = la_sizes(B, T, H, d_k, d_v, alpha_per_head, dtype, varlen != 0);
   if (rc != CKDA_OK) return rc;
   if (B == 0) return 0;
-  return (int64_t)ckda::la_bwd_simt_workspace_bytes(d_k, d_v, B, T, H, varlen != 0,
-                                                    alpha_per_head != 0);
+  const bool vl = varlen != 0, ph = alpha_per_head != 0;
+  return (int64_t)(ckda::la_bwd_tc_supported(dtype, d_k, d_v, B, T, H, vl)
+                       ? ckda::la_bwd_tc_workspace_bytes(d_k, d_v, B, T, H, vl, ph)
+                       : ckda::la_bwd_simt_workspace_bytes(d_k, d_v, B, T, H, vl, ph));
 }
 
 int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
@@ -192,9 +202,15 @@ int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float
   if (rc != CKDA_OK) return rc;
   int* status = ckda::status_word();
   if (status == nullptr) return CKDA_ERR_CUDA;
-  const cudaError_t err = ckda::launch_la_bwd_simt(
-      dtype, d_k, d_v, q, k, v, alpha, alpha_per_head, S0, cu_seqlens, dO, dS_final, dq, dk, dv,
-      dalpha, dS0, workspace, B, T, H, status, static_cast<cudaStream_t>(stream));
+  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  const cudaError_t err =
+      ckda::la_bwd_tc_supported(dtype, d_k, d_v, B, T, H, varlen)
+          ? ckda::launch_la_bwd_tc(d_k, d_v, q, k, v, alpha, alpha_per_head, S0, cu_seqlens, dO,
+                                   dS_final, dq, dk, dv, dalpha, dS0, workspace, B, T, H, status,
+                                   st_)
+          : ckda::launch_la_bwd_simt(dtype, d_k, d_v, q, k, v, alpha, alpha_per_head, S0,
+                                     cu_seqlens, dO, dS_final, dq, dk, dv, dalpha, dS0, workspace,
+                                     B, T, H, status, st_);
   return err == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 

@@ -1,0 +1,1026 @@
+// Backward of head-decay linear attention on the tensor cores (tcgen05): bf16
+// inputs, d_k = 128, d_v 64 or 128 (sm_100a).
+//
+// Per chunk of C = 128 tokens, S the state at its start, G the adjoint of the
+// state at its end, D(i, j) = a_{j+1} .. a_i (zero for j > i):
+//   E = D o (dO V^T),  P = D o (Q K^T)
+//   dQ = E K   + diag(pre) dO S^T        pre_i = a_0 .. a_i
+//   dK = E^T Q + diag(suf) V G^T         suf_j = a_{j+1} .. a_{C-1}
+//   dV = P^T dO + diag(suf) K G
+//   da_t = sum_{i >= t > j} D(i, t) D(t-1, j) W_ij + head_t X_t + tail_t Y_t
+//          + head_t tail_t <S, G>,   W = (Q K^T) o (dO V^T)
+// with X_t = sum_{i >= t} D(i, t) x_i, x_i = q_i . (dO S^T)_i,
+// Y_t = sum_{j < t} D(t-1, j) y_j, y_j = v_j . (K G)_j, head_t = a_0 .. a_{t-1},
+// tail_t = suf_t: nothing is divided by a decay.
+//
+// Two kernels:
+//  1. la_states_kernel walks every sequence's chunks forward for S and
+//     backward for G and leaves both at every chunk's bound (fp32).  It is the
+//     forward's state path alone: one product per chunk, diag(w) V split into
+//     three bf16 terms side by side.
+//  2. la_chunk_kernel takes one (chunk, head) at a time, all of them in
+//     parallel.  S and G enter their products as three bf16 terms each
+//     (V G^T: one), because x, y and so the decays' gradient keep fp32
+//     accuracy; dq, dk, dv are rounded to bf16 in the end, and E, P once on
+//     the way.
+// Bound by HBM bandwidth and by the chunk kernel's chain of phases; the two
+// states of 64 KB per (chunk, head), written and read once, are more than half
+// of the traffic.
+#include "la_tc.cuh"
+
+namespace ckda {
+namespace la {
+
+using namespace sm100;
+
+namespace bw {
+
+constexpr int C = 128;
+constexpr int DK = 128;
+constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
+
+// A state in the workspace: columns in groups of four, [d_v / 4][128 rows][4],
+// so that a warp whose lanes are rows reads and writes whole lines.
+__host__ __device__ constexpr size_t state_floats(int dv) { return (size_t)DK * dv; }
+
+// ---- kernel 1: states at the chunks' bounds -------------------------------------------
+
+namespace st {
+
+constexpr int BV = 64;
+constexpr int kHalf = BV / 2;
+constexpr uint32_t OFF_A = 0;                     // k or q [128][128]
+constexpr uint32_t OFF_B = 32768;                 // v or do [128][64]
+constexpr uint32_t OFF_VW = OFF_B + 16384;        // diag(w) of it, three terms
+constexpr uint32_t OFF_DEC = OFF_VW + 3 * 16384;  // 2 x {a[128], sufW[128], tot[4]}
+constexpr uint32_t kDecBytes = 1024 + 16;
+constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
+constexpr uint32_t B_A = 0, B_B = 8, B_VW = 16, B_D = 24, B_DEC = 32, B_DECE = 48;
+constexpr uint32_t OFF_MISC = OFF_BAR + 64;
+constexpr uint32_t kSmem = OFF_MISC + 16;
+constexpr uint32_t kTmemCols = 256;
+constexpr int kThreads = 352;
+
+struct Args {
+  Decay al;
+  const float *S0, *dSf;
+  float *Sk, *Gk;  // kept states
+  float* dS0;      // or NULL
+  const int32_t* cu;
+  int n_seqs, T, H, DV;
+  int* status;
+};
+
+__global__ void __launch_bounds__(kThreads, 2)
+la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                 const Args p) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if ((sb & 1023u) != 0) {
+    set_status(p.status, CKDA_ERR_CUDA);
+    return;
+  }
+  // block index: column slice, direction, head, sequence (longest first)
+  const int slices = p.DV / BV;
+  int b = blockIdx.x;
+  const int j0 = (b % slices) * BV;
+  b /= slices;
+  const bool rev = b & 1;
+  b >>= 1;
+  const int h = b % p.H;
+  const int n = longest_first(p.cu, p.n_seqs, b / p.H, reinterpret_cast<int*>(sm + OFF_MISC + 4));
+  const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
+  if (!sr.ok) return;
+  const uint32_t bar = sb + OFF_BAR;
+  const CUtensorMap* tm_a = rev ? &tm_q : &tm_k;
+  const CUtensorMap* tm_b = rev ? &tm_do : &tm_v;
+  if (tid == 0) {
+    mbar_init(bar + B_A, 1);
+    mbar_init(bar + B_B, 1);
+    mbar_init(bar + B_VW, 8);
+    mbar_init(bar + B_D, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(bar + B_DEC + 8 * i, 1);
+      mbar_init(bar + B_DECE + 8 * i, 8);
+    }
+    fence_mbar_init();
+    prefetch_tmap(tm_a);
+    prefetch_tmap(tm_b);
+  }
+  if (warp == 0) {
+    tmem_alloc(sb + OFF_MISC, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem =
+      __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC), 0);
+  const int nck = __shfl_sync(0xffffffffu, (int)((sr.end - sr.begin + C - 1) / C), 0);
+  // the it-th chunk taken
+  auto chunk = [&](int it) -> int { return rev ? nck - 1 - it : it; };
+  auto tok = [&](int it) -> int64_t { return sr.begin + (int64_t)chunk(it) * C; };
+  auto len_of = [&](int it) -> int {
+    const int64_t left = sr.end - tok(it);
+    return left < C ? (int)left : C;
+  };
+  auto wait = [&](uint32_t off, uint32_t par) -> bool {
+    return mbar_wait_small(bar + off, par & 1u, kWaitNs);
+  };
+  auto arrive = [&](uint32_t off) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar + off);
+  };
+  const float* dec0 = reinterpret_cast<const float*>(sm + OFF_DEC);
+  auto decs = [&](int it) { return dec0 + (it & 1) * (kDecBytes / 4); };
+  bool ok = true;
+  bool open_a = false, open_b = false, mma_open = false;
+  uint32_t par_last = 0;
+
+  if (warp < 8) {
+    // ---- state: row r of d_k, half of the slice's columns ------------------------------
+    const int q4 = warp & 3, hf = warp >> 2;
+    const int r = 32 * q4 + lane;
+    const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
+    const size_t unit = (size_t)n * p.H + h, stsz = state_floats(p.DV);
+    const size_t at = (size_t)r * p.DV + j0 + kHalf * hf;
+    float S[kHalf];
+    {
+      const float* src = rev ? p.dSf : p.S0;
+#pragma unroll
+      for (int e = 0; e < kHalf; e += 4) {
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (src != nullptr) x = *reinterpret_cast<const float4*>(src + unit * stsz + at + e);
+        S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
+      }
+    }
+    float* kept = (rev ? p.Gk : p.Sk) + (size_t)(j0 + kHalf * hf) * DK + 4 * r;
+    const int64_t slot0 = slot_of(p.cu, n, p.T, C);
+    float gamma = 1.f;
+#pragma unroll 1
+    for (int it = 0; it <= nck; ++it) {
+      if (it > 0) {
+        if (!(ok = wait(B_D, it - 1))) break;
+        tc_fence_after();
+        const float2 g2 = make_float2(gamma, gamma);
+#pragma unroll
+        for (int e = 0; e < kHalf; e += 8) {
+          float x[8], y[8], z[8];
+          tmem_ld8(row + kHalf * hf + e, x);
+          tmem_ld8(row + BV + kHalf * hf + e, y);
+          tmem_ld8(row + 2 * BV + kHalf * hf + e, z);
+          tmem_ld_wait();
+#pragma unroll
+          for (int u = 0; u < 8; u += 2) {
+            const float2 d = add2(make_float2(x[u], x[u + 1]),
+                                  add2(make_float2(y[u], y[u + 1]), make_float2(z[u], z[u + 1])));
+            const float2 s = fma2(g2, make_float2(S[e + u], S[e + u + 1]), d);
+            S[e + u] = s.x;
+            S[e + u + 1] = s.y;
+          }
+        }
+      }
+      if (it == nck) break;
+      {
+        float* o = kept + ((size_t)(slot0 + chunk(it)) * p.H + h) * stsz;
+#pragma unroll
+        for (int e = 0; e < kHalf; e += 4)
+          *reinterpret_cast<float4*>(o + (size_t)e * DK) =
+              make_float4(S[e], S[e + 1], S[e + 2], S[e + 3]);
+      }
+      const int len = len_of(it);
+      if (!(ok = wait(B_DEC + 8 * (it & 1), it >> 1))) break;
+      const float* dc = decs(it);
+      const float4 tot = *reinterpret_cast<const float4*>(dc + 256);
+      float wgt;
+      if (rev)
+        wgt = warp_prefix(dc[r], lane) * (q4 > 0 ? tot.x : 1.f) * (q4 > 1 ? tot.y : 1.f) *
+              (q4 > 2 ? tot.z : 1.f);
+      else
+        wgt = dc[128 + r] * (q4 < 1 ? tot.y : 1.f) * (q4 < 2 ? tot.z : 1.f) *
+              (q4 < 3 ? tot.w : 1.f);
+      gamma = (tot.x * tot.y) * (tot.z * tot.w);
+      arrive(B_DECE + 8 * (it & 1));
+      if (!(ok = wait(B_B, it))) break;
+      if (len < C && !(ok = wait(B_A, it))) break;
+      if (r < len) {
+        const float2 w2 = make_float2(wgt, wgt);
+#pragma unroll 1
+        for (int h2 = 0; h2 < 2; ++h2) {
+          const uint32_t o0 = sw128_chunk(r, kHalf * hf + 16 * h2, 128);
+          const uint32_t o1 = o0 ^ 16u;  // the next 16 bytes under the swizzle
+          const uint4 ra = *reinterpret_cast<const uint4*>(sm + OFF_B + o0);
+          const uint4 rb = *reinterpret_cast<const uint4*>(sm + OFF_B + o1);
+          const uint32_t in[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+          uint32_t t1[8], t2[8], t3[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) split3(in[e], w2, &t1[e], &t2[e], &t3[e]);
+          uint8_t* d = sm + OFF_VW;
+          *reinterpret_cast<uint4*>(d + o0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+          *reinterpret_cast<uint4*>(d + o1) = make_uint4(t1[4], t1[5], t1[6], t1[7]);
+          *reinterpret_cast<uint4*>(d + 16384 + o0) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+          *reinterpret_cast<uint4*>(d + 16384 + o1) = make_uint4(t2[4], t2[5], t2[6], t2[7]);
+          *reinterpret_cast<uint4*>(d + 32768 + o0) = make_uint4(t3[0], t3[1], t3[2], t3[3]);
+          *reinterpret_cast<uint4*>(d + 32768 + o1) = make_uint4(t3[4], t3[5], t3[6], t3[7]);
+        }
+      } else {
+        // what lies past the sequence's end takes no part, finite or not
+        const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int c8 = 0; c8 < kHalf / 8; ++c8)
+          for (int e = 0; e < 3; ++e)
+            *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 +
+                                      sw128_chunk(r, kHalf * hf + 8 * c8, 128)) = z;
+#pragma unroll 1
+        for (int c8 = 0; c8 < DK / 16; ++c8)
+          *reinterpret_cast<uint4*>(sm + OFF_A + sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+      arrive(B_VW);
+    }
+    if (ok && rev && p.dS0 != nullptr) store_cols<kHalf>(p.dS0 + unit * stsz + at, S);
+  } else if (warp == 8) {
+    // ---- MMA (the whole warp waits, one lane issues) ---------------------------------------
+    const uint64_t d_a = smem_desc(sb + OFF_A, 16384, 1024, kSwizzle128);
+    const uint64_t d_vw = smem_desc(sb + OFF_VW, 16384, 1024, kSwizzle128);
+    constexpr uint32_t id = idesc_bf16(128, 3 * BV, 1, 1);
+#pragma unroll 1
+    for (int it = 0; it < nck; ++it) {
+      if (!(ok = wait(B_VW, it) && wait(B_A, it))) break;
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          mma_f16(tmem, d_a + 128 * kk, d_vw + 128 * kk, id, kk > 0 ? 1u : 0u);
+        mma_commit(bar + B_D);
+      }
+      __syncwarp();
+      mma_open = true;
+      par_last = it;
+    }
+  } else if (warp == 9) {
+    // ---- loads: b of the next chunk once its rows are converted, a once the
+    // product is done (the two blocks of an SM cover for one another) -----------------------
+    if (lane == 0) {
+#pragma unroll 1
+      for (int it = 0; it < nck; ++it) {
+        const int t = (int)tok(it);
+        if (it > 0 && !(ok = wait(B_VW, it - 1))) break;
+        mbar_expect_tx(bar + B_B, 16384);
+        tma_load_2d(sb + OFF_B, tm_b, h * p.DV + j0, t, bar + B_B);
+        open_b = true;
+        par_last = it;
+        if (it + 1 < nck) {
+          const int t1 = (int)tok(it + 1);
+          tma_prefetch_2d(tm_a, h * DK, t1);
+          tma_prefetch_2d(tm_a, h * DK + 64, t1);
+          tma_prefetch_2d(tm_b, h * p.DV + j0, t1);
+        }
+        if (it > 0 && !(ok = wait(B_D, it - 1))) break;
+        mbar_expect_tx(bar + B_A, 32768);
+        tma_load_2d(sb + OFF_A, tm_a, h * DK, t, bar + B_A);
+        tma_load_2d(sb + OFF_A + 16384, tm_a, h * DK + 64, t, bar + B_A);
+        open_a = true;
+      }
+      if (!ok) {  // give the loads in flight their time
+        if (open_b) mbar_wait_small(bar + B_B, par_last & 1u, kWaitNs);
+        if (open_a && par_last > 0) mbar_wait_small(bar + B_A, (par_last - 1) & 1u, kWaitNs);
+      }
+    }
+  } else {
+    // ---- decays ---------------------------------------------------------------------------
+    auto load = [&](int it, float* a) {
+      const int len = it < nck ? len_of(it) : 0;
+      const int64_t t0 = it < nck ? tok(it) : 0;
+#pragma unroll
+      for (int bk = 0; bk < 4; ++bk) {
+        const int t = 32 * bk + lane;
+        a[bk] = t < len ? p.al.now(t0 + t, h) : 1.f;
+      }
+    };
+    float a[4], nx[4];
+    load(0, a);
+#pragma unroll 1
+    for (int it = 0; it < nck; ++it) {
+      load(it + 1, nx);
+      if (it >= 2 && !(ok = wait(B_DECE + 8 * (it & 1), (it >> 1) - 1))) break;
+      float* o = reinterpret_cast<float*>(sm + OFF_DEC) + (it & 1) * (kDecBytes / 4);
+#pragma unroll
+      for (int bk = 0; bk < 4; ++bk) {
+        const float pw = warp_prefix(a[bk], lane), sw = warp_suffix(a[bk], lane);
+        o[32 * bk + lane] = a[bk];
+        o[128 + 32 * bk + lane] = sw;
+        if (lane == 31) o[256 + bk] = pw;
+        a[bk] = nx[bk];
+      }
+      arrive(B_DEC + 8 * (it & 1));
+    }
+  }
+  if (!ok) {
+    set_status(p.status, CKDA_ERR_DEVICE_TIMEOUT);
+    if (warp == 8 && mma_open) mbar_wait_small(bar + B_D, par_last & 1u, kWaitNs);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace st
+
+// ---- kernel 2: the gradients of one (chunk, head) ----------------------------------------
+
+namespace ck {
+
+constexpr uint32_t OFF_Q = 0, OFF_K = 32768;         // [128][128] bf16, two 64-column atoms
+constexpr uint32_t OFF_V = 65536, OFF_DO = 98304;    // [128][DV]
+constexpr uint32_t OFF_E = 131072, OFF_P = 163840;   // first two terms of S, then E and P
+constexpr uint32_t OFF_T = 196608;                   // third term of S, then the terms of G
+constexpr uint32_t OFF_F = 229376;                   // floats, below
+// decays; sufW; block products; <S, G> by warp; x by column half; column sums
+// of the six row and column blocks below the diagonal
+constexpr uint32_t F_A = 0, F_SW = 128, F_TOT = 256, F_Z = 260, F_X = 268, F_COL = 524;
+// later in their places: y by column half, the sums within the chunk
+constexpr uint32_t F_Y0 = F_COL, F_Y1 = F_SW, F_IN = F_X + 128;
+constexpr uint32_t OFF_BAR = OFF_F + 4 * 716;
+constexpr uint32_t B_LD = 0;    // tiles loaded
+constexpr uint32_t B_SC = 8;    // scores complete (tensor core)
+constexpr uint32_t B_DS = 16;   // dO S^T complete
+constexpr uint32_t B_G = 24;    // a term of G is done with (three times per unit)
+constexpr uint32_t B_FIN = 32;  // the gradients complete
+constexpr uint32_t OFF_MISC = OFF_BAR + 40;
+constexpr uint32_t kSmem = OFF_MISC + 16;
+static_assert(kSmem <= 232448, "shared memory");
+
+constexpr uint32_t TM_S1 = 0, TM_S2 = 128;           // Q K^T, dO V^T
+constexpr uint32_t TM_DV = 0, TM_DK = 128, TM_DQ = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kCompute = 256;
+constexpr int kThreads = kCompute + 32;
+
+struct Args {
+  Decay al;
+  const float *Sk, *Gk;
+  __nv_bfloat16 *dq, *dk, *dv;
+  float* da;
+  const int32_t* cu;
+  int n_seqs, T, H;
+  int64_t units;  // slots * H
+  int* status;
+};
+
+// V_t = c_t V_{t-1} + b_t over 128 positions, four per lane; V_{-1} = 0.
+__device__ __forceinline__ void lin_scan(const float* c, const float* b, float* v, int lane) {
+  float A = c[0], B = b[0];
+#pragma unroll
+  for (int e = 1; e < 4; ++e) {
+    B = fmaf(c[e], B, b[e]);
+    A *= c[e];
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float pa = __shfl_up_sync(0xffffffffu, A, o), pb = __shfl_up_sync(0xffffffffu, B, o);
+    if (lane >= o) {
+      B = fmaf(A, pb, B);
+      A *= pa;
+    }
+  }
+  float x = __shfl_up_sync(0xffffffffu, B, 1);
+  if (lane == 0) x = 0.f;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    x = fmaf(c[e], x, b[e]);
+    v[e] = x;
+  }
+}
+
+// A row's N columns of an accumulator times f, in place; returns the row's
+// product (before f) with the same columns of a 128-byte-swizzled bf16 tile.
+template <int N>
+__device__ __forceinline__ float scale_rows(uint32_t addr, float f, const uint8_t* tile, int i,
+                                            int col) {
+  float s = 0.f;
+#pragma unroll 1
+  for (int e = 0; e < N; e += 16) {
+    float x[16];
+    tmem_ld16(addr + e, x);
+    tmem_ld_wait();
+    if (tile != nullptr) {
+#pragma unroll
+      for (int o = 0; o < 16; o += 8) {
+        const uint4 r = *reinterpret_cast<const uint4*>(tile + sw128_chunk(i, col + e + o, 128));
+        const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          s = fmaf(x[o + 2 * t], lo_f(w[t]), fmaf(x[o + 2 * t + 1], hi_f(w[t]), s));
+      }
+    }
+    uint32_t y[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t) y[t] = __float_as_uint(f * x[t]);
+    tmem_st16(addr + e, y);
+  }
+  tmem_st_wait();
+  return s;
+}
+
+template <int DV>
+__global__ void __launch_bounds__(kThreads, 1)
+la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
+                const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
+                const __grid_constant__ CUtensorMap tm_dv, const Args p) {
+  extern __shared__ __align__(1024) uint8_t sm[];
+  const uint32_t sb = smem_u32(sm);
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if ((sb & 1023u) != 0) {
+    set_status(p.status, CKDA_ERR_CUDA);
+    return;
+  }
+  const uint32_t bar = sb + OFF_BAR;
+  float* F = reinterpret_cast<float*>(sm + OFF_F);
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) mbar_init(bar + 8 * i, 1);
+    fence_mbar_init();
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+    prefetch_tmap(&tm_do);
+  }
+  if (warp == 0) {
+    tmem_alloc(sb + OFF_MISC, kTmemCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem =
+      __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC), 0);
+  auto wait = [&](uint32_t off, uint32_t par) -> bool {
+    return mbar_wait_small(bar + off, par & 1u, kWaitNs);
+  };
+  // the unit's first token, its tokens and its head; 0 tokens: no such chunk
+  auto decode = [&](int64_t u, int64_t* t0, int* h) -> int {
+    *h = (int)(u % p.H);
+    int n, c;
+    if (!slot_chunk(p.cu, p.n_seqs, p.T, C, u / p.H, &n, &c)) return 0;
+    const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
+    if (!sr.ok) return 0;
+    *t0 = sr.begin + (int64_t)c * C;
+    const int64_t left = sr.end - *t0;
+    return left < C ? (int)left : C;
+  };
+  auto load = [&](int64_t t0, int h) {
+    const int t = (int)t0;
+    mbar_expect_tx(bar + B_LD, 65536 + 2 * 128 * DV * 2);
+    for (int x = 0; x < DK; x += 64) {
+      tma_load_2d(sb + OFF_Q + 256 * x, &tm_q, h * DK + x, t, bar + B_LD);
+      tma_load_2d(sb + OFF_K + 256 * x, &tm_k, h * DK + x, t, bar + B_LD);
+    }
+    for (int x = 0; x < DV; x += 64) {
+      tma_load_2d(sb + OFF_DO + 256 * x, &tm_do, h * DV + x, t, bar + B_LD);
+      tma_load_2d(sb + OFF_V + 256 * x, &tm_v, h * DV + x, t, bar + B_LD);
+    }
+  };
+
+  const bool mma_warp = warp == 8;
+  const uint64_t q_k = smem_desc(sb + OFF_Q, 16, 1024, kSwizzle128);      // K-major
+  const uint64_t q_m = smem_desc(sb + OFF_Q, 16384, 1024, kSwizzle128);   // MN-major
+  constexpr uint64_t kTile = 32768 >> 4;
+  // tiles by index: 0 Q, 1 K, 2 V, 3 dO, 4 E, 5 P, 6 T
+  auto km = [&](int tile, int kk) { return q_k + tile * kTile + 1024 * (kk >> 2) + 2 * (kk & 3); };
+  auto mn = [&](int tile, int kk) { return q_m + tile * kTile + 128 * kk; };
+
+  // compute threads: row (token or d_k) and column half
+  const int w4 = warp & 3, hf = (warp >> 2) & 1;
+  const int i = 32 * w4 + lane;
+  const uint32_t row = tmem + ((uint32_t)(32 * w4) << 16);
+  bool ok = true, loaded = false;
+  uint32_t ld_par = 0, issued = 0, issued_par = 0;  // the MMA warp's last load and commit
+  int64_t t0 = 0, t0n = 0;
+  int h = 0, hn = 0;
+  int64_t u = blockIdx.x;
+  int len = 0;
+  for (; u < p.units; u += gridDim.x)
+    if ((len = decode(u, &t0, &h)) > 0) break;
+  if (u < p.units && mma_warp && lane == 0) load(t0, h);
+  if (u < p.units) loaded = true;
+  uint32_t ph = 0, g3 = 0;
+#pragma unroll 1
+  while (u < p.units) {
+    // the next unit with tokens
+    int64_t un = u + gridDim.x;
+    int lenn = 0;
+    for (; un < p.units; un += gridDim.x)
+      if ((lenn = decode(un, &t0n, &hn)) > 0) break;
+
+    float X[DV / 2];  // a row of S, later of G: what is left of it to split
+    const float4* Sg = reinterpret_cast<const float4*>(p.Sk + u * state_floats(DV)) +
+                       (size_t)(DV / 8 * hf) * DK + i;
+    const float4* Gg = reinterpret_cast<const float4*>(p.Gk + u * state_floats(DV)) +
+                       (size_t)(DV / 8 * hf) * DK + i;
+    // one bf16 term of X into a tile, X keeps the rest
+    auto term = [&](uint32_t off) {
+#pragma unroll
+      for (int e = 0; e < DV / 2; e += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          w[x] = pack_bf16x2(X[e + 2 * x], X[e + 2 * x + 1]);
+          X[e + 2 * x] -= lo_f(w[x]);
+          X[e + 2 * x + 1] -= hi_f(w[x]);
+        }
+        *reinterpret_cast<uint4*>(sm + off + sw128_chunk(i, DV / 2 * hf + e, 128)) =
+            make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    };
+    float z = 0.f;
+    if (!mma_warp) {
+#pragma unroll
+      for (int e = 0; e < DV / 8; ++e) {
+        const float4 x = __ldcs(Sg + (size_t)e * DK), y = __ldg(Gg + (size_t)e * DK);
+        X[4 * e] = x.x; X[4 * e + 1] = x.y; X[4 * e + 2] = x.z; X[4 * e + 3] = x.w;
+        z = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, z))));
+      }
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    }
+    // the last unit's gradients have left their tiles
+    if (mma_warp && lane == 0) bulk_wait_read_all();
+    __syncthreads();
+    if (!mma_warp) {
+      if (lane == 0) F[F_Z + warp] = z;
+      term(OFF_E);
+      term(OFF_P);
+      term(OFF_T);
+      fence_proxy_async_smem();
+      if (warp < 4) {  // decays
+        const float a = i < len ? p.al.at(t0 + i, h) : 1.f;
+        const float pw = warp_prefix(a, lane);
+        F[F_A + i] = a;
+        F[F_SW + i] = warp_suffix(a, lane);
+        if (lane == 31) F[F_TOT + w4] = pw;
+      }
+    } else {
+      if ((ok = wait(B_LD, ph)) && elect_one()) {
+        constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_S1, km(0, kk), km(1, kk), id, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < DV / 16; ++kk) mma_f16(tmem + TM_S2, km(3, kk), km(2, kk), id, kk > 0);
+        mma_commit(bar + B_SC);
+      }
+      __syncwarp();
+      issued = B_SC;
+      issued_par = ph;
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+
+    const float4 tot = *reinterpret_cast<const float4*>(F + F_TOT);
+    const float pw = i < 128 ? warp_prefix(F[F_A + (i & 127)], lane) : 1.f;
+    const float pre = pw * (w4 > 0 ? tot.x : 1.f) * (w4 > 1 ? tot.y : 1.f) * (w4 > 2 ? tot.z : 1.f);
+    const float suf = F[F_SW + i] * (w4 < 1 ? tot.y : 1.f) * (w4 < 2 ? tot.z : 1.f) *
+                      (w4 < 3 ? tot.w : 1.f);
+    if (mma_warp) {
+      // dO S^T, the three terms of S one after another
+      if (elect_one()) {
+        constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
+#pragma unroll 1
+        for (int e = 0; e < 3; ++e)
+#pragma unroll
+          for (int kk = 0; kk < DV / 16; ++kk)
+            mma_f16(tmem + TM_DQ, km(3, kk), km(4 + e, kk), id, (e > 0 || kk > 0) ? 1u : 0u);
+        mma_commit(bar + B_DS);
+      }
+      __syncwarp();
+      issued = B_DS;
+      issued_par = ph;
+      ok = wait(B_DS, ph);
+    } else {
+      // what lies past the sequence's end takes no part, finite or not (the
+      // scores' products may read these rows before or after: rows and
+      // columns that are masked)
+      ok = wait(B_LD, ph);
+      if (ok && i >= len) {
+        const uint4 zz = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+        for (int e = 0; e < DK / 16; ++e) {
+          *reinterpret_cast<uint4*>(sm + OFF_Q + sw128_chunk(i, DK / 2 * hf + 8 * e, 128)) = zz;
+          *reinterpret_cast<uint4*>(sm + OFF_K + sw128_chunk(i, DK / 2 * hf + 8 * e, 128)) = zz;
+        }
+#pragma unroll 1
+        for (int e = 0; e < DV / 16; ++e) {
+          *reinterpret_cast<uint4*>(sm + OFF_V + sw128_chunk(i, DV / 2 * hf + 8 * e, 128)) = zz;
+          *reinterpret_cast<uint4*>(sm + OFF_DO + sw128_chunk(i, DV / 2 * hf + 8 * e, 128)) = zz;
+        }
+        fence_proxy_async_smem();
+      }
+      // G's rows on their way while the products run
+      if (ok) {
+#pragma unroll
+        for (int e = 0; e < DV / 8; ++e) {
+          const float4 y = __ldcs(Gg + (size_t)e * DK);
+          X[4 * e] = y.x; X[4 * e + 1] = y.y; X[4 * e + 2] = y.z; X[4 * e + 3] = y.w;
+        }
+        ok = wait(B_SC, ph) && wait(B_DS, ph);
+        tc_fence_after();
+      }
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+
+    float intra = 0.f;
+    // ---- E and P, the decays' sums within the chunk; x and dO S^T scaled; the
+    // first term of G ----------------------------------------------------------------------
+    if (!mma_warp) {
+      term(OFF_T);
+      fence_proxy_async_smem();
+      const bool in = i < len;
+      if (hf == 0) {
+        // R(t) = sum_{j < t} D(t - 1, j) W_ij runs along the row; column t of
+        // the block then sums D(i, t) R(t) over its rows
+        float R = 0.f;
+#pragma unroll 1
+        for (int J = 0; J <= w4; ++J) {
+          float d = pw;  // decays between block J and this row's
+          if (w4 > 1 && J < 1) d *= tot.y;
+          if (w4 > 2 && J < 2) d *= tot.z;
+          // D(i, t) in the diagonal block, from t = i down
+          float dd[32];
+          if (J == w4) {
+            float run = 1.f;
+            const float a = F[F_A + i];
+#pragma unroll
+            for (int t = 31; t >= 0; --t) {
+              const float at = __shfl_sync(0xffffffffu, a, t);
+              dd[t] = t <= lane ? run : 0.f;
+              run = t <= lane ? run * at : run;
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 32; ++t) dd[t] = d * F[F_SW + 32 * J + t];
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 16) {
+            float s1[16], s2[16];
+            tmem_ld16(row + TM_S1 + 32 * J + e, s1);
+            tmem_ld16(row + TM_S2 + 32 * J + e, s2);
+            tmem_ld_wait();
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+              const bool on = in && (J < w4 || e + t <= lane);
+              const float w = on ? s1[t] * s2[t] : 0.f;
+              dd[e + t] = on ? dd[e + t] * R : 0.f;
+              R = fmaf(F[F_A + 32 * J + e + t], R, w);
+            }
+          }
+          // lane t gets the sum of dd[t] over the lanes
+#pragma unroll
+          for (int o = 16; o >= 1; o >>= 1) {
+            const bool up = lane & o;
+#pragma unroll
+            for (int t = 0; t < o; ++t) {
+              const float give = up ? dd[t] : dd[t + o];
+              const float keep = up ? dd[t + o] : dd[t];
+              dd[t] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+            }
+          }
+          const float cs = dd[0];
+          if (J == w4)
+            intra = cs;
+          else
+            F[F_COL + 32 * (w4 * (w4 - 1) / 2 + J) + lane] = cs;
+        }
+      } else {
+#pragma unroll 1
+        for (int J = 0; J < 4; ++J) {
+          float s1[32], s2[32];
+          if (J <= w4) {
+            tmem_ld32(row + TM_S1 + 32 * J, s1);
+            tmem_ld32(row + TM_S2 + 32 * J, s2);
+            tmem_ld_wait();
+            if (J == w4) {
+              float run = 1.f;
+              const float a = F[F_A + i];
+#pragma unroll
+              for (int t = 31; t >= 0; --t) {
+                const float at = __shfl_sync(0xffffffffu, a, t);
+                const bool on = in && t <= lane;
+                s1[t] = on ? s1[t] * run : 0.f;
+                s2[t] = on ? s2[t] * run : 0.f;
+                run = t <= lane ? run * at : run;
+              }
+            } else {
+              float d = pw;
+              if (w4 > 1 && J < 1) d *= tot.y;
+              if (w4 > 2 && J < 2) d *= tot.z;
+#pragma unroll
+              for (int t = 0; t < 32; ++t) {
+                const float f = d * F[F_SW + 32 * J + t];
+                s1[t] = in ? s1[t] * f : 0.f;
+                s2[t] = in ? s2[t] * f : 0.f;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 32; ++t) s1[t] = s2[t] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            *reinterpret_cast<uint4*>(sm + OFF_P + sw128_chunk(i, 32 * J + e, 128)) = pack8(s1 + e);
+            *reinterpret_cast<uint4*>(sm + OFF_E + sw128_chunk(i, 32 * J + e, 128)) = pack8(s2 + e);
+          }
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+
+    // ---- K G and V G^T with G's first term; x; diag(pre) dO S^T ---------------------------
+    constexpr uint32_t id_kg = idesc_bf16(128, DV, 0, 1), id_128 = idesc_bf16(128, 128, 0, 0);
+    if (mma_warp) {
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, kk > 0);
+#pragma unroll
+        for (int kk = 0; kk < DV / 16; ++kk)
+          mma_f16(tmem + TM_DK, km(2, kk), km(6, kk), id_128, kk > 0);
+        mma_commit(bar + B_G);
+      }
+      __syncwarp();
+      issued = B_G;
+      issued_par = g3;
+      ok = wait(B_G, g3);
+    } else {
+      if (hf == 0) {
+#pragma unroll
+        for (int w = 1; w < 4; ++w)
+          if (w > w4) intra += F[F_COL + 32 * (w * (w - 1) / 2 + w4) + lane];
+      }
+      const float x = scale_rows<64>(row + TM_DQ + 64 * hf, pre, sm + OFF_Q, i, 64 * hf);
+      F[F_X + 128 * hf + i] = i < len ? x : 0.f;
+      ok = wait(B_G, g3);
+      term(OFF_T);
+      fence_proxy_async_smem();
+      tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+
+    // ---- second term; E K -----------------------------------------------------------------
+    if (mma_warp) {
+      tc_fence_after();
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
+        mma_commit(bar + B_G);
+        constexpr uint32_t id = idesc_bf16(128, 128, 0, 1);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DQ, km(4, kk), mn(1, kk), id, 1u);
+      }
+      __syncwarp();
+      issued = B_G;
+      issued_par = g3 + 1;
+      ok = wait(B_G, g3 + 1);
+    } else {
+      if (hf == 0) {
+        F[F_X + i] += F[F_X + 128 + i];
+        F[F_IN + i] = intra;
+      }
+      ok = wait(B_G, g3 + 1);
+      term(OFF_T);
+      fence_proxy_async_smem();
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+
+    // ---- third term; y; diag(suf) K G, diag(suf) V G^T --------------------------------------
+    if (mma_warp) {
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
+        mma_commit(bar + B_G);
+      }
+      __syncwarp();
+      issued = B_G;
+      issued_par = g3 + 2;
+      ok = wait(B_G, g3 + 2);
+    } else {
+      ok = wait(B_G, g3 + 2);
+      tc_fence_after();
+      const float y = scale_rows<DV / 2>(row + TM_DV + DV / 2 * hf, suf, sm + OFF_V, i, DV / 2 * hf);
+      F[(hf ? F_Y1 : F_Y0) + i] = i < len ? y : 0.f;
+      scale_rows<64>(row + TM_DK + 64 * hf, suf, nullptr, i, 0);
+      tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+
+    // ---- P^T dO, E^T Q; the decays' gradient ------------------------------------------------
+    if (mma_warp) {
+      tc_fence_after();
+      if (elect_one()) {
+        constexpr uint32_t id_dv = idesc_bf16(128, DV, 1, 1), id_dk = idesc_bf16(128, 128, 1, 1);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, mn(5, kk), mn(3, kk), id_dv, 1u);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DK, mn(4, kk), mn(0, kk), id_dk, 1u);
+        mma_commit(bar + B_FIN);
+      }
+      __syncwarp();
+      issued = B_FIN;
+      issued_par = ph;
+      ok = wait(B_FIN, ph);
+      loaded = false;
+      if (ok && un < p.units) {
+        if (lane == 0) load(t0n, hn);
+        loaded = true;
+        ld_par = ph ^ 1u;
+      }
+    } else {
+      if (warp == 0) {
+        float a[4], c[4], b[4], v[4], y[4], hd[4], tl[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 4 * lane + e, s = 127 - t;
+          a[e] = F[F_A + t];
+          y[e] = F[F_Y0 + t] + F[F_Y1 + t];
+          c[e] = t > 0 ? F[F_A + s + 1] : 0.f;
+          b[e] = F[F_X + s];
+        }
+        lin_scan(c, b, v, lane);  // X, from the end
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) F[F_X + 127 - 4 * lane - e] = v[e];
+        lin_scan(a, y, v, lane);  // Y of the next position
+        float Y = __shfl_up_sync(0xffffffffu, v[3], 1);
+        if (lane == 0) Y = 0.f;
+        const float all = (a[0] * a[1]) * (a[2] * a[3]);
+        float up = __shfl_up_sync(0xffffffffu, warp_prefix(all, lane), 1);
+        float down = warp_suffix(all, lane);
+        if (lane == 0) up = 1.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          hd[e] = up;
+          up *= a[e];
+          tl[3 - e] = down;
+          down *= a[3 - e];
+        }
+        float zz = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) zz += F[F_Z + e];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 4 * lane + e;
+          float g = F[F_IN + t];
+          g = fmaf(hd[e], F[F_X + t], g);
+          g = fmaf(tl[e], e > 0 ? v[e - 1] : Y, g);
+          g = fmaf(hd[e] * tl[e], zz, g);
+          if (t < len) p.da[(t0 + t) * p.H + h] = g;
+        }
+      }
+      ok = wait(B_FIN, ph);
+      tc_fence_after();
+      // the gradients' rows: whole chunks leave by TMA from the tiles of E, P
+      // and G's terms, a partial one row by row
+      auto give = [&](uint32_t col, uint32_t off, __nv_bfloat16* g, int D, int n0, int nn) {
+#pragma unroll 1
+        for (int e = n0; e < n0 + nn; e += 32) {
+          float x[32];
+          tmem_ld32(row + col + e, x);
+          tmem_ld_wait();
+          if (len == C) {
+#pragma unroll
+            for (int o = 0; o < 32; o += 8)
+              *reinterpret_cast<uint4*>(sm + off + sw128_chunk(i, e + o, 128)) = pack8(x + o);
+          } else if (i < len) {
+            store_cols<32>(g + ((t0 + i) * p.H + h) * D + e, x);
+          }
+        }
+      };
+      if (ok) {
+        give(TM_DQ, OFF_E, p.dq, DK, 64 * hf, 64);
+        give(TM_DK, OFF_P, p.dk, DK, 64 * hf, 64);
+        give(TM_DV, OFF_T, p.dv, DV, DV / 2 * hf, DV / 2);
+      }
+      fence_proxy_async_smem();
+      tc_fence_before();
+    }
+    ok = __syncthreads_and(ok);
+    if (!ok) break;
+    if (mma_warp && lane == 0 && len == C) {
+      const int t = (int)t0;
+      for (int x = 0; x < DK; x += 64) {
+        tma_store_2d(&tm_dq, sb + OFF_E + 256 * x, h * DK + x, t);
+        tma_store_2d(&tm_dk, sb + OFF_P + 256 * x, h * DK + x, t);
+      }
+      for (int x = 0; x < DV; x += 64) tma_store_2d(&tm_dv, sb + OFF_T + 256 * x, h * DV + x, t);
+      bulk_commit();
+    }
+    tc_fence_after();
+    u = un;
+    len = lenn;
+    t0 = t0n;
+    h = hn;
+    ph ^= 1u;
+    g3 += 3;
+  }
+  if (mma_warp && lane == 0) bulk_wait_all();
+  if (!ok) {
+    set_status(p.status, CKDA_ERR_DEVICE_TIMEOUT);
+    // loads and products in flight get their time
+    if (mma_warp) {
+      if (loaded) wait(B_LD, ld_par);
+      if (issued != 0) wait(issued, issued_par);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmemCols);
+}
+
+}  // namespace ck
+
+}  // namespace bw
+}  // namespace la
+
+bool la_bwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen) {
+  const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
+  return dtype == CKDA_BF16 && dk == la::bw::DK && (dv == 64 || dv == 128) && rows > 0 &&
+         rows <= 0x7fffffffull - la::bw::C && (uint64_t)H * (dk > dv ? dk : dv) <= 0x7fffffffull;
+}
+
+size_t la_bwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen,
+                                 bool per_head) {
+  const size_t slots = (size_t)la::chunk_slots(varlen, n_seqs, T, la::bw::C);
+  const size_t tokens = varlen ? (size_t)T : (size_t)n_seqs * T;
+  return 2 * slots * H * dk * dv * 4 + (per_head ? (tokens * H * 4 + 255) / 256 * 256 : 0);
+}
+
+cudaError_t launch_la_dalpha_sum(const float* part, float* da, int64_t tokens, int H,
+                                 cudaStream_t stream);
+
+cudaError_t launch_la_bwd_tc(int dk_, int dv_, const void* q, const void* k, const void* v,
+                             const float* alpha, int per_head, const float* S0, const int32_t* cu,
+                             const void* dO, const float* dSf, void* dq, void* dk, void* dv,
+                             float* dalpha, float* dS0, void* ws, int n_seqs, int T, int H,
+                             int* status, cudaStream_t stream) {
+  using namespace la;
+  const bool varlen = cu != nullptr;
+  const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
+  const int64_t slots = chunk_slots(varlen, n_seqs, T, bw::C);
+  float* Sk = static_cast<float*>(ws);
+  float* Gk = Sk + (size_t)slots * H * dk_ * dv_;
+  float* part = per_head ? Gk + (size_t)slots * H * dk_ * dv_ : dalpha;
+  const Decay al{alpha, H, per_head};
+  CUtensorMap mq, mk, mv, mo, nq, nk, nv;
+  const uint64_t ck_ = (uint64_t)H * dk_, cv = (uint64_t)H * dv_;
+  if (!bf16_map(&mq, q, ck_, rows, bw::C) || !bf16_map(&mk, k, ck_, rows, bw::C) ||
+      !bf16_map(&mv, v, cv, rows, bw::C) || !bf16_map(&mo, dO, cv, rows, bw::C) ||
+      !bf16_map(&nq, dq, ck_, rows, bw::C) || !bf16_map(&nk, dk, ck_, rows, bw::C) ||
+      !bf16_map(&nv, dv, cv, rows, bw::C))
+    return cudaErrorInvalidValue;
+  cudaError_t e;
+  {
+    auto ks = bw::st::la_states_kernel;
+    if ((e = max_smem<10>(ks, bw::st::kSmem)) != cudaSuccess) return e;
+    const bw::st::Args a{al, S0, dSf, Sk, Gk, dS0, cu, n_seqs, T, H, dv_, status};
+    ks<<<(unsigned)n_seqs * H * 2 * (dv_ / bw::st::BV), bw::st::kThreads, bw::st::kSmem, stream>>>(
+        mq, mk, mv, mo, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const bw::ck::Args a{al,
+                       Sk,
+                       Gk,
+                       static_cast<__nv_bfloat16*>(dq),
+                       static_cast<__nv_bfloat16*>(dk),
+                       static_cast<__nv_bfloat16*>(dv),
+                       part,
+                       cu,
+                       n_seqs,
+                       T,
+                       H,
+                       slots * H,
+                       status};
+  const unsigned grid = (unsigned)(a.units < 148 ? a.units : 148);
+  if (dv_ == 128) {
+    auto kc = bw::ck::la_chunk_kernel<128>;
+    if ((e = max_smem<11>(kc, bw::ck::kSmem)) != cudaSuccess) return e;
+    kc<<<grid, bw::ck::kThreads, bw::ck::kSmem, stream>>>(mq, mk, mv, mo, nq, nk, nv, a);
+  } else {
+    auto kc = bw::ck::la_chunk_kernel<64>;
+    if ((e = max_smem<12>(kc, bw::ck::kSmem)) != cudaSuccess) return e;
+    kc<<<grid, bw::ck::kThreads, bw::ck::kSmem, stream>>>(mq, mk, mv, mo, nq, nk, nv, a);
+  }
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return per_head ? launch_la_dalpha_sum(part, dalpha, (int64_t)rows, H, stream) : cudaSuccess;
+}
+
+}  // namespace ckda
