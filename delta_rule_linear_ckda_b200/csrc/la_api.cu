@@ -276,7 +276,7 @@ int ckda_qk_norm_rope(const void* q, const void* k, const float* wq, const float
   if (overlap(out[0], out[1])) return CKDA_ERR_INVALID_ARG;
   const ckda::qkn::Args p{q, k, wq, wk, positions, inv_freq, q_out, k_out, nullptr, nullptr,
                           nullptr, q_stride, k_stride, tokens, Hq, Hk, d, rot, interleaved, 0,
-                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps};
+                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps, 0};
   const cudaError_t err =
       ckda::launch_qk_norm_fwd(p, dtype, out_dtype, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
@@ -329,7 +329,7 @@ int ckda_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const f
   const ckda::qkn::Args p{q, k, wq, wk, positions, inv_freq, dq, dk, dq_out, dk_out,
                           sums ? static_cast<float*>(workspace) : nullptr, q_stride, k_stride,
                           tokens, Hq, Hk, d, rot, interleaved, 0,
-                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps};
+                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps, 0};
   if (tokens == 0 && !sums) return CKDA_OK;
   const cudaError_t err =
       ckda::launch_qk_norm_bwd(p, dtype, dwq, dwk, static_cast<cudaStream_t>(stream));

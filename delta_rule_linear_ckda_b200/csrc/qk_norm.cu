@@ -12,21 +12,22 @@
 // Both are bound by HBM bandwidth: a row is read once and written once.  A
 // thread owns two units of G adjacent channels (G = 8: 16 bytes of bf16) that
 // hold whole pairs, so that the turn needs no exchange between threads; the
-// 16 / G ... d / (2 G) threads of a row are adjacent lanes and sum over it by
-// shuffles.  A CTA takes whole tokens, queries' and keys' heads alike, so
-// the angles' sines and cosines are computed once per token and pair and
-// shared through shared memory, while the first rows are on their way.
+// d / (2 G) threads of a row are adjacent lanes and sum over it by shuffles.
+// A warp takes some heads of one token, queries' and keys' alike, so that a
+// thread computes the sines and cosines of its own pairs once for all of them
+// and no barrier stands between the rows; the next rows are requested before
+// the present ones are used.
 //
-// Angles: the position times the fp32 frequency is exact in 64 bits up to
-// 53 bits, so the reduction to turns in [-1/2, 1/2] is made there and only
-// the reduced angle is rounded to 32 bits (error below 2^-24 of a turn at
-// any int32 position).
+// Angles: the turns, position * inv_freq / (2 pi), and their reduction to
+// [-1/2, 1/2] are computed in 64 bits (error below 2^-50 of the turns), and
+// only the reduced angle is rounded to 32 bits, to 2^-25 of a turn.
 #include "qk_norm.cuh"
 
 namespace ckda {
 namespace qkn {
 
-constexpr int kThreads = 256;
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
 
 template <typename T, int G>
 __device__ __forceinline__ void load_unit(const T* p, float* x);
@@ -83,24 +84,20 @@ __device__ __forceinline__ void units(int c, int rot, int interleaved, int* a, i
 
 // The pairs of a thread's two units turned by (cs.x, sgn * cs.y).
 template <int G>
-__device__ __forceinline__ void turn(float* x, float* y, const float2* cs, int a, int interleaved,
+__device__ __forceinline__ void turn(float* x, float* y, const float2* cs, int interleaved,
                                      float sgn) {
-  if (!interleaved) {
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      const float2 w = cs[a + i];
-      const float s = sgn * w.y, x0 = x[i], y0 = y[i];
-      x[i] = x0 * w.x - y0 * s;
-      y[i] = y0 * w.x + x0 * s;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 2 * G; i += 2) {
-      float* z = i < G ? x + i : y + i - G;
-      const float2 w = cs[(a + i) >> 1];
-      const float s = sgn * w.y, x0 = z[0], y0 = z[1];
-      z[0] = x0 * w.x - y0 * s;
-      z[1] = y0 * w.x + x0 * s;
+  for (int i = 0; i < G; ++i) {
+    const float c = cs[i].x, s = sgn * cs[i].y;
+    if (!interleaved) {
+      const float x0 = x[i], y0 = y[i];
+      x[i] = x0 * c - y0 * s;
+      y[i] = y0 * c + x0 * s;
+    } else {
+      float* z = 2 * i < G ? x + 2 * i : y + 2 * i - G;
+      const float x0 = z[0], y0 = z[1];
+      z[0] = x0 * c - y0 * s;
+      z[1] = y0 * c + x0 * s;
     }
   }
 }
@@ -112,139 +109,164 @@ __device__ __forceinline__ float inv_norm(float ss, const Args& p) {
   return m == 0.f ? 0.f : rsqrtf(m);
 }
 
-// cos and sin of pos[t] * inv_freq[p] for `nt` tokens from t0.
-__device__ __forceinline__ void angles(const Args& p, int64_t t0, int nt, float2* cs) {
-  const int half = p.rot / 2;
+// cos and sin of pos[t] * inv_freq for a thread's G pairs (unit offset a).
+template <int G>
+__device__ __forceinline__ void angles(const Args& p, int64_t t, int a, float2* cs) {
   constexpr double kInv2Pi = 0.15915494309189533577;
-  for (int e = threadIdx.x; e < nt * half; e += kThreads) {
-    const int t = e / half, i = e - t * half;
-    double turns = (double)__ldg(p.pos + t0 + t) * (double)__ldg(p.inv_freq + i) * kInv2Pi;
+  const double pos = (double)__ldg(p.pos + t) * kInv2Pi;
+  const float* f = p.inv_freq + (p.interleaved ? a / 2 : a);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    double turns = pos * (double)__ldg(f + i);
     turns -= rint(turns);
-    float s, c;
-    sincospif(2.0f * (float)turns, &s, &c);
-    cs[e] = make_float2(c, s);
+    sincospif(2.0f * (float)turns, &cs[i].y, &cs[i].x);
   }
+}
+
+// A warp's rows: heads [h0, h1) of token t, RPW of them at a time.
+struct Unit {
+  int64_t t;
+  int h0, h1;
+};
+
+__device__ __forceinline__ Unit unit_of(const Args& p, int64_t u) {
+  Unit x;
+  const int groups = (p.Hq + p.Hk + p.heads_warp - 1) / p.heads_warp;
+  x.t = u / groups;
+  x.h0 = (int)(u - x.t * groups) * p.heads_warp;
+  x.h1 = min(p.Hq + p.Hk, x.h0 + p.heads_warp);
+  return x;
+}
+
+template <int G>
+struct Weights {
+  float q[2 * G], k[2 * G];
+  __device__ __forceinline__ void load(const Args& p, int a, int b) {
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) {
+      const int ch = i < G ? a + i : b + i - G;
+      q[i] = p.wq != nullptr ? __ldg(p.wq + ch) : 1.f;
+      k[i] = p.wk != nullptr ? __ldg(p.wk + ch) : 1.f;
+    }
+  }
+};
+
+template <typename T, int D>
+__device__ __forceinline__ const T* row_in(const Args& p, int64_t t, int hh) {
+  return hh < p.Hq ? static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)hh * D
+                   : static_cast<const T*>(p.k) + t * p.k_stride + (int64_t)(hh - p.Hq) * D;
+}
+
+// A row's offset in a contiguous [tokens, heads, D] tensor of its own.
+template <int D>
+__device__ __forceinline__ int64_t row_at(const Args& p, int64_t t, int hh) {
+  return hh < p.Hq ? (t * p.Hq + hh) * D : (t * p.Hk + hh - p.Hq) * D;
 }
 
 template <typename Tin, typename Tout, int D, int G>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
-  constexpr int TPR = D / (2 * G);       // threads per row
-  constexpr int RPP = kThreads / TPR;    // rows per pass
-  extern __shared__ float2 cs[];
-  const int heads = p.Hq + p.Hk;
-  const int c = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  constexpr int TPR = D / (2 * G);  // threads per row
+  constexpr int RPW = 32 / TPR;     // rows per warp and pass
+  const int lane = threadIdx.x & 31;
+  const int c = lane % TPR, rg = lane / TPR;
+  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
+  if (u >= p.units) return;
+  const Unit un = unit_of(p, u);
   int a, b;
   bool trn;
   units<G>(c, p.rot, p.interleaved, &a, &b, &trn);
-  float wq[2 * G], wk[2 * G];
-#pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
-    const int ch = i < G ? a + i : b + i - G;
-    wq[i] = p.wq != nullptr ? __ldg(p.wq + ch) : 1.f;
-    wk[i] = p.wk != nullptr ? __ldg(p.wk + ch) : 1.f;
-  }
-  const int64_t t0 = (int64_t)blockIdx.x * p.tok_cta;
-  const int nt = (int)min((int64_t)p.tok_cta, p.tokens - t0);
-  const int nrows = nt * heads;
-  // (every thread of a row's lanes takes the same trips, so the shuffles meet)
-  for (int r0 = 0; r0 < nrows; r0 += RPP) {
-    const int row = r0 + rg;
-    const bool ok = row < nrows;
-    const int t = ok ? row / heads : 0, hh = ok ? row - t * heads : 0;
-    const bool isq = hh < p.Hq;
-    float x[G], y[G];
+  float x[G], y[G];
+  auto fetch = [&](int hh) {
 #pragma unroll
     for (int i = 0; i < G; ++i) x[i] = y[i] = 0.f;
-    if (ok) {
-      const Tin* src = isq ? static_cast<const Tin*>(p.q) + (t0 + t) * p.q_stride + (int64_t)hh * D
-                           : static_cast<const Tin*>(p.k) + (t0 + t) * p.k_stride +
-                                 (int64_t)(hh - p.Hq) * D;
+    if (hh < un.h1) {
+      const Tin* src = row_in<Tin, D>(p, un.t, hh);
       load_unit<Tin, G>(src + a, x);
       load_unit<Tin, G>(src + b, y);
     }
-    if (r0 == 0) {
-      if (p.rot > 0) angles(p, t0, nt, cs);
-      __syncthreads();
+  };
+  fetch(un.h0 + rg);
+  Weights<G> w;
+  w.load(p, a, b);
+  float2 cs[G];
+  if (trn) angles<G>(p, un.t, a, cs);
+  // (every lane takes the same trips, so the shuffles meet)
+  for (int r0 = un.h0; r0 < un.h1; r0 += RPW) {
+    const int hh = r0 + rg;
+    const bool isq = hh < p.Hq;
+    float u0[G], v0[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      u0[i] = x[i];
+      v0[i] = y[i];
     }
+    fetch(hh + RPW);
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < G; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+    for (int i = 0; i < G; ++i) ss = fmaf(u0[i], u0[i], fmaf(v0[i], v0[i], ss));
 #pragma unroll
     for (int o = TPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
     const float r = inv_norm(ss, p);
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      x[i] *= r * (isq ? wq[i] : wk[i]);
-      y[i] *= r * (isq ? wq[G + i] : wk[G + i]);
+      u0[i] *= r * (isq ? w.q[i] : w.k[i]);
+      v0[i] *= r * (isq ? w.q[G + i] : w.k[G + i]);
     }
-    if (trn) turn<G>(x, y, cs + t * (p.rot / 2), a, p.interleaved, 1.f);
-    if (ok) {
-      Tout* dst = isq ? static_cast<Tout*>(p.oq) + ((t0 + t) * p.Hq + hh) * D
-                      : static_cast<Tout*>(p.ok) + ((t0 + t) * p.Hk + hh - p.Hq) * D;
-      store_unit<Tout, G>(dst + a, x);
-      store_unit<Tout, G>(dst + b, y);
+    if (trn) turn<G>(u0, v0, cs, p.interleaved, 1.f);
+    if (hh < un.h1) {
+      Tout* dst = static_cast<Tout*>(isq ? p.oq : p.ok) + row_at<D>(p, un.t, hh);
+      store_unit<Tout, G>(dst + a, u0);
+      store_unit<Tout, G>(dst + b, v0);
     }
   }
 }
 
-// The CTAs walk the token groups with a stride of the grid, so that each adds
-// its rows' shares of dw up in registers and leaves one partial sum per
+// The warps walk the units with a stride of the grid, so that each adds its
+// rows' shares of dw up in registers and a CTA leaves one partial sum per
 // weight; dw_kernel adds those in a fixed order.
-template <typename T, int D, int G>
+template <typename T, int D, int G, bool SUMS>
 __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
   constexpr int TPR = D / (2 * G);
-  constexpr int RPP = kThreads / TPR;
-  extern __shared__ float2 cs[];
-  __shared__ float sw[2][kThreads / 32][D];
-  const int heads = p.Hq + p.Hk;
-  const int c = threadIdx.x % TPR, rg = threadIdx.x / TPR;
+  constexpr int RPW = 32 / TPR;
+  __shared__ float sw[2][kWarps][D];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = lane % TPR, rg = lane / TPR;
   int a, b;
   bool trn;
   units<G>(c, p.rot, p.interleaved, &a, &b, &trn);
-  float wq[2 * G], wk[2 * G], dwq[2 * G], dwk[2 * G];
+  Weights<G> w;
+  w.load(p, a, b);
+  float dwq[2 * G], dwk[2 * G];
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
-    const int ch = i < G ? a + i : b + i - G;
-    wq[i] = p.wq != nullptr ? __ldg(p.wq + ch) : 1.f;
-    wk[i] = p.wk != nullptr ? __ldg(p.wk + ch) : 1.f;
-    dwq[i] = dwk[i] = 0.f;
-  }
-  for (int64_t t0 = (int64_t)blockIdx.x * p.tok_cta; t0 < p.tokens;
-       t0 += (int64_t)gridDim.x * p.tok_cta) {
-    const int nt = (int)min((int64_t)p.tok_cta, p.tokens - t0);
-    const int nrows = nt * heads;
-    for (int r0 = 0; r0 < nrows; r0 += RPP) {
-      const int row = r0 + rg;
-      const bool ok = row < nrows;
-      const int t = ok ? row / heads : 0, hh = ok ? row - t * heads : 0;
-      const bool isq = hh < p.Hq;
-      float x[G], y[G], u[G], w[G];
+  for (int i = 0; i < 2 * G; ++i) dwq[i] = dwk[i] = 0.f;
+  for (int64_t uu = (int64_t)blockIdx.x * kWarps + warp; uu < p.units;
+       uu += (int64_t)gridDim.x * kWarps) {
+    const Unit un = unit_of(p, uu);
+    float2 cs[G];
+    if (trn) angles<G>(p, un.t, a, cs);
+    for (int r0 = un.h0; r0 < un.h1; r0 += RPW) {
+      const int hh = r0 + rg;
+      const bool ok = hh < un.h1, isq = hh < p.Hq;
+      float x[G], y[G], u[G], v[G];
 #pragma unroll
-      for (int i = 0; i < G; ++i) x[i] = y[i] = u[i] = w[i] = 0.f;
-      const int64_t at = isq ? ((t0 + t) * p.Hq + hh) * D : ((t0 + t) * p.Hk + hh - p.Hq) * D;
+      for (int i = 0; i < G; ++i) x[i] = y[i] = u[i] = v[i] = 0.f;
+      const int64_t at = row_at<D>(p, un.t, hh);
       if (ok) {
-        const T* src = isq ? static_cast<const T*>(p.q) + (t0 + t) * p.q_stride + (int64_t)hh * D
-                           : static_cast<const T*>(p.k) + (t0 + t) * p.k_stride +
-                                 (int64_t)(hh - p.Hq) * D;
+        const T* src = row_in<T, D>(p, un.t, hh);
         const T* gr = static_cast<const T*>(isq ? p.gq : p.gk) + at;
         load_unit<T, G>(src + a, x);
         load_unit<T, G>(src + b, y);
         load_unit<T, G>(gr + a, u);
-        load_unit<T, G>(gr + b, w);
+        load_unit<T, G>(gr + b, v);
       }
-      if (r0 == 0 && p.rot > 0) {
-        __syncthreads();  // the last tokens' angles have been read
-        angles(p, t0, nt, cs);
-        __syncthreads();
-      }
-      if (trn) turn<G>(u, w, cs + t * (p.rot / 2), a, p.interleaved, -1.f);
+      if (trn) turn<G>(u, v, cs, p.interleaved, -1.f);
       float ss = 0.f, dot = 0.f;
 #pragma unroll
       for (int i = 0; i < G; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        dot = fmaf(x[i] * u[i], isq ? wq[i] : wk[i], dot);
-        dot = fmaf(y[i] * w[i], isq ? wq[G + i] : wk[G + i], dot);
+        dot = fmaf(x[i] * u[i], isq ? w.q[i] : w.k[i], dot);
+        dot = fmaf(y[i] * v[i], isq ? w.q[G + i] : w.k[G + i], dot);
       }
 #pragma unroll
       for (int o = TPR / 2; o >= 1; o >>= 1) {
@@ -253,53 +275,51 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
       }
       const float r = inv_norm(ss, p);
       const float m = p.c * r * r * r * dot;
-      if (p.part != nullptr && ok) {
+      if (SUMS) {  // (a lane without a row adds zeros)
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          const float e = u[i] * (x[i] * r), f = w[i] * (y[i] * r);
-          if (isq) {
-            dwq[i] += e;
-            dwq[G + i] += f;
-          } else {
-            dwk[i] += e;
-            dwk[G + i] += f;
-          }
+          const float e = u[i] * (x[i] * r), f = v[i] * (y[i] * r);
+          dwq[i] += isq ? e : 0.f;
+          dwq[G + i] += isq ? f : 0.f;
+          dwk[i] += isq ? 0.f : e;
+          dwk[G + i] += isq ? 0.f : f;
         }
       }
 #pragma unroll
       for (int i = 0; i < G; ++i) {
-        u[i] = fmaf(r * (isq ? wq[i] : wk[i]), u[i], -m * x[i]);
-        w[i] = fmaf(r * (isq ? wq[G + i] : wk[G + i]), w[i], -m * y[i]);
+        u[i] = fmaf(r * (isq ? w.q[i] : w.k[i]), u[i], -m * x[i]);
+        v[i] = fmaf(r * (isq ? w.q[G + i] : w.k[G + i]), v[i], -m * y[i]);
       }
       if (ok) {
         T* dst = static_cast<T*>(isq ? p.oq : p.ok) + at;
         store_unit<T, G>(dst + a, u);
-        store_unit<T, G>(dst + b, w);
+        store_unit<T, G>(dst + b, v);
       }
     }
   }
-  if (p.part == nullptr) return;
-  // lanes c, c + TPR, ... of a warp hold the same channels
+  if constexpr (SUMS) {
+    // lanes c, c + TPR, ... of a warp hold the same channels
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) {
+    for (int i = 0; i < 2 * G; ++i) {
 #pragma unroll
-    for (int o = TPR; o < 32; o <<= 1) {
-      dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-      dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
+      for (int o = TPR; o < 32; o <<= 1) {
+        dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
+        dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
+      }
+      const int ch = i < G ? a + i : b + i - G;
+      if (lane < TPR) {
+        sw[0][warp][ch] = dwq[i];
+        sw[1][warp][ch] = dwk[i];
+      }
     }
-    const int ch = i < G ? a + i : b + i - G;
-    if ((threadIdx.x & 31) < TPR) {
-      sw[0][threadIdx.x / 32][ch] = dwq[i];
-      sw[1][threadIdx.x / 32][ch] = dwk[i];
-    }
-  }
-  __syncthreads();
-  for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
-    const int which = e / D, ch = e - which * D;
-    float s = 0.f;
+    __syncthreads();
+    for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
+      const int which = e / D, ch = e - which * D;
+      float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) s += sw[which][w][ch];
-    p.part[((size_t)blockIdx.x * 2 + which) * D + ch] = s;
+      for (int k = 0; k < kWarps; ++k) s += sw[which][k][ch];
+      p.part[((size_t)blockIdx.x * 2 + which) * D + ch] = s;
+    }
   }
 }
 
@@ -323,35 +343,35 @@ __global__ void __launch_bounds__(256) dw_kernel(const float* __restrict__ part,
   }
 }
 
-// Tokens per CTA: enough rows for every thread, at most 32 tokens (so that
-// the angles of 64 pairs each take 16 KB of shared memory).
-static int tokens_per_cta(int heads, int rpp) {
-  int t = (rpp + heads - 1) / heads;
-  return t < 1 ? 1 : (t > 32 ? 32 : t);
-}
-
 constexpr int kBwdGrid = 148 * 4;
 
-static int bwd_grid(int64_t tokens, int tok_cta) {
-  const int64_t groups = (tokens + tok_cta - 1) / tok_cta;
-  return (int)(groups < kBwdGrid ? groups : kBwdGrid);
+// Heads of a token that one warp takes: all of them (in up to 8 passes) when
+// the tokens alone give every SM 16 warps, else one pass's.
+static void plan(Args* p, int rpw) {
+  const int heads = p->Hq + p->Hk;
+  const int64_t all = p->tokens * ((heads + 8 * rpw - 1) / (8 * rpw));
+  p->heads_warp = all >= 148 * 16 ? 8 * rpw : rpw;
+  p->units = p->tokens * ((heads + p->heads_warp - 1) / p->heads_warp);
 }
 
 template <typename Tin, typename Tout, int D, int G>
 static cudaError_t launch_fwd(Args p, cudaStream_t st) {
-  p.tok_cta = tokens_per_cta(p.Hq + p.Hk, kThreads / (D / (2 * G)));
-  const unsigned grid = (unsigned)((p.tokens + p.tok_cta - 1) / p.tok_cta);
-  fwd_kernel<Tin, Tout, D, G><<<grid, kThreads, (size_t)p.tok_cta * p.rot / 2 * 8, st>>>(p);
+  plan(&p, 32 / (D / (2 * G)));
+  fwd_kernel<Tin, Tout, D, G><<<(unsigned)((p.units + kWarps - 1) / kWarps), kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D, int G>
 static cudaError_t launch_bwd(Args p, float* dwq, float* dwk, cudaStream_t st) {
-  p.tok_cta = tokens_per_cta(p.Hq + p.Hk, kThreads / (D / (2 * G)));
-  const int grid = bwd_grid(p.tokens, p.tok_cta);  // 0 without tokens: dw = 0
+  plan(&p, 32 / (D / (2 * G)));
+  const int64_t ctas = (p.units + kWarps - 1) / kWarps;
+  const int grid = (int)(ctas < kBwdGrid ? ctas : kBwdGrid);  // 0 without tokens: dw = 0
   cudaError_t e = cudaSuccess;
   if (grid > 0) {
-    bwd_kernel<T, D, G><<<grid, kThreads, (size_t)p.tok_cta * p.rot / 2 * 8, st>>>(p);
+    if (p.part != nullptr)
+      bwd_kernel<T, D, G, true><<<grid, kThreads, 0, st>>>(p);
+    else
+      bwd_kernel<T, D, G, false><<<(unsigned)ctas, kThreads, 0, st>>>(p);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && p.part != nullptr) {

@@ -17,8 +17,9 @@ struct Args {
   int64_t q_stride, k_stride;
   int64_t tokens;
   int Hq, Hk, d, rot, interleaved;
-  int tok_cta;            // tokens a CTA takes at a time
+  int heads_warp;         // heads of a token that one warp takes (set at launch, as units)
   float c, eps;
+  int64_t units;          // warps' shares
 };
 
 }  // namespace qkn
