@@ -6,6 +6,7 @@ on a non-zero status.  All arithmetic happens in the CUDA kernels.
 """
 from __future__ import annotations
 
+import functools
 import math
 from typing import Optional, Tuple
 
@@ -545,6 +546,29 @@ def sfda_decode_step(q, k, v, alpha, theta, beta, S, out=None, out_dtype=None) -
 
 # ---- head-decay linear attention ------------------------------------------------
 
+# A call's checks and its launch take about 10 us on the host, as long as the
+# smallest kernels: the usual case is one expression per tensor (``_need`` words
+# the error), and the current device is set only when it is another one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _check(t, name, dtype, dev):
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.device == dev
+            and t.is_contiguous() and dev.type == "cuda"):
+        _need(t, name, dtype, dev)
+
+
+def _stream_of(dev):
+    return _raw_stream(dev.index) if _raw_stream is not None else _stream_ptr(dev)
+
+
+def _call(fn, dev, *args):
+    """``fn(*args, stream)`` with ``dev`` as the current device."""
+    if torch.cuda.current_device() == dev.index:
+        return fn(*args, _stream_of(dev))
+    with torch.cuda.device(dev):
+        return fn(*args, _stream_of(dev))
+
 
 def _la_inputs(q, k, v, alpha, cu_seqlens):
     """Checks the inputs; returns (B, T, H, dk, dv, per_head) as passed to the ABI."""
@@ -552,14 +576,14 @@ def _la_inputs(q, k, v, alpha, cu_seqlens):
     if q.dtype not in _DT:
         raise TypeError("q, k, v must be float32 or bfloat16")
     for name, t in (("q", q), ("k", k), ("v", v)):
-        _need(t, name, q.dtype, dev)
-    _need(alpha, "alpha", torch.float32, dev)
+        _check(t, name, q.dtype, dev)
+    _check(alpha, "alpha", torch.float32, dev)
     if cu_seqlens is None:
         if q.dim() != 4:
             raise ValueError("q must be [B, T, H, dk]")
         B, T, H, dk = q.shape
     else:
-        _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+        _check(cu_seqlens, "cu_seqlens", torch.int32, dev)
         if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
             raise ValueError("cu_seqlens must be [N + 1]")
         if q.dim() == 4:
@@ -579,11 +603,12 @@ def _la_inputs(q, k, v, alpha, cu_seqlens):
 
 def _la_state(t, name, shape, dev):
     if t is not None:
-        _need(t, name, torch.float32, dev)
+        _check(t, name, torch.float32, dev)
         if t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}")
 
 
+@functools.lru_cache(maxsize=1024)
 def la_workspace_bytes(B, T, H, dk, dv, dtype=torch.bfloat16, varlen=False) -> int:
     """Scratch bytes ``la_fwd_chunked`` needs for these sizes."""
     rc = _lib.load().ckda_la_fwd_workspace_bytes(B, T, H, dk, dv, _DT[dtype], 1 if varlen else 0)
@@ -610,7 +635,7 @@ def la_fwd_chunked(q, k, v, alpha, S0=None, cu_seqlens=None, out=None, S_final=N
     if out is None:
         out = torch.empty(v.shape, dtype=out_dtype, device=dev)
     else:
-        _need(out, "out", out_dtype, dev)
+        _check(out, "out", out_dtype, dev)
         if out.shape != v.shape:
             raise ValueError("out must have v's shape")
     if return_final and S_final is None:
@@ -621,17 +646,18 @@ def la_fwd_chunked(q, k, v, alpha, S0=None, cu_seqlens=None, out=None, S_final=N
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, dev)
-    with torch.cuda.device(dev):
-        rc = _lib.load().ckda_la_fwd_chunked(
-            _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(out), _p(S_final), B, T, H,
-            dk, dv, 1 if per_head else 0, _DT[q.dtype], _DT[out_dtype], _p(workspace),
-            0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+        _check(workspace, "workspace", torch.uint8, dev)
+    rc = _call(
+        _lib.load().ckda_la_fwd_chunked, dev,
+        _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(out), _p(S_final), B, T, H,
+        dk, dv, 1 if per_head else 0, _DT[q.dtype], _DT[out_dtype], _p(workspace),
+        0 if workspace is None else workspace.numel())
     if rc != 0:
         raise CKDAError(rc, "ckda_la_fwd_chunked")
     return out, S_final
 
 
+@functools.lru_cache(maxsize=1024)
 def la_bwd_workspace_bytes(B, T, H, dk, dv, alpha_per_head=False, dtype=torch.bfloat16,
                            varlen=False) -> int:
     """Scratch bytes ``la_bwd_chunked`` needs for these sizes."""
@@ -652,7 +678,7 @@ def la_bwd_chunked(q, k, v, alpha, dO, S0=None, dS_final=None, cu_seqlens=None, 
     ``grads`` may supply preallocated output tensors under the same names."""
     dev = q.device
     B, T, H, dk, dv, per_head = _la_inputs(q, k, v, alpha, cu_seqlens)
-    _need(dO, "dO", q.dtype, dev)
+    _check(dO, "dO", q.dtype, dev)
     if dO.shape != v.shape:
         raise ValueError("dO must have v's shape")
     st = (B, H, dk, dv)
@@ -668,7 +694,7 @@ def la_bwd_chunked(q, k, v, alpha, dO, S0=None, dS_final=None, cu_seqlens=None, 
         if t is None:
             t = torch.empty(shape, dtype=dtype, device=dev)
         else:
-            _need(t, name, dtype, dev)
+            _check(t, name, dtype, dev)
             if t.shape != shape:
                 raise ValueError(f"{name} must be {list(shape)}")
         g[name] = t
@@ -678,13 +704,13 @@ def la_bwd_chunked(q, k, v, alpha, dO, S0=None, dS_final=None, cu_seqlens=None, 
     if workspace is None and need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, dev)
-    with torch.cuda.device(dev):
-        rc = _lib.load().ckda_la_bwd_chunked(
-            _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(dO), _p(dS_final),
-            _p(g["dq"]), _p(g["dk"]), _p(g["dv"]), _p(g["dalpha"]), _p(g["dS0"]), B, T, H, dk, dv,
-            1 if per_head else 0, _DT[q.dtype], _p(workspace),
-            0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+        _check(workspace, "workspace", torch.uint8, dev)
+    rc = _call(
+        _lib.load().ckda_la_bwd_chunked, dev,
+        _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(dO), _p(dS_final),
+        _p(g["dq"]), _p(g["dk"]), _p(g["dv"]), _p(g["dalpha"]), _p(g["dS0"]), B, T, H, dk, dv,
+        1 if per_head else 0, _DT[q.dtype], _p(workspace),
+        0 if workspace is None else workspace.numel())
     if rc != 0:
         raise CKDAError(rc, "ckda_la_bwd_chunked")
     return g
@@ -694,17 +720,34 @@ def la_decode_step(q, k, v, alpha, S, out=None, out_dtype=None) -> torch.Tensor:
     """One token of head-decay linear attention in place on ``S`` ``[B, H, dk, dv]``
     (``ckda_la_decode_step``): alpha (fp32) ``[B, H]``, or ``[H]`` for one decay per
     head; otherwise as ``decode_step``."""
-    B, H, dk = q.shape
-    per_head = isinstance(alpha, torch.Tensor) and alpha.dim() == 1
-    dev, B, H, dk, dv = _decode_checks(q, k, v, S,
-                                       (("alpha", alpha, (H,) if per_head else (B, H)),))
-    out, out_dtype = _decode_out(q, v, out, out_dtype, dev)
-    if out.shape != v.shape:
-        raise ValueError("out must have v's shape")
-    with torch.cuda.device(dev):
-        rc = _lib.load().ckda_la_decode_step(
-            _p(q), _p(k), _p(v), _p(alpha), _p(S), _p(out), B, H, dk, dv, 1 if per_head else 0,
-            _DT[q.dtype], _DT[out_dtype], _stream_ptr(dev))
+    dev, dtype = q.device, q.dtype
+    if dtype not in _DT:
+        raise TypeError("q, k, v must be float32 or bfloat16")
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _check(t, name, dtype, dev)
+    _check(S, "S", torch.float32, dev)
+    _check(alpha, "alpha", torch.float32, dev)
+    if S.dim() != 4 or q.shape != S.shape[:3] or k.shape != q.shape or \
+            v.shape != S.shape[:2] + S.shape[3:]:
+        raise ValueError("q, k must be [B, H, dk], v [B, H, dv] and S [B, H, dk, dv]")
+    B, H, dk, dv = S.shape
+    per_head = alpha.dim() == 1
+    if alpha.shape != ((H,) if per_head else (B, H)):
+        raise ValueError("alpha must be [B, H] or [H]")
+    if out_dtype is None:
+        out_dtype = out.dtype if out is not None else dtype
+    if out_dtype not in _DT:
+        raise TypeError("out_dtype must be float32 or bfloat16")
+    if out is None:
+        out = torch.empty_like(v, dtype=out_dtype)
+    else:
+        _check(out, "out", out_dtype, dev)
+        if out.shape != v.shape:
+            raise ValueError("out must have v's shape")
+    rc = _call(
+        _lib.load().ckda_la_decode_step, dev,
+        _p(q), _p(k), _p(v), _p(alpha), _p(S), _p(out), B, H, dk, dv, 1 if per_head else 0,
+        _DT[q.dtype], _DT[out_dtype])
     if rc != 0:
         raise CKDAError(rc, "ckda_la_decode_step")
     return out
@@ -756,15 +799,15 @@ def _qk_inputs(q, k, wq, wk, positions, inv_freq, norm):
     lead, (Hq, d), Hk = q.shape[:-2], q.shape[-2:], k.shape[-2]
     for name, w in (("wq", wq), ("wk", wk)):
         if w is not None:
-            _need(w, name, torch.float32, dev)
+            _check(w, name, torch.float32, dev)
             if w.shape != (d,):
                 raise ValueError(f"{name} must be [{d}]")
     rot = 0
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq come together")
     if positions is not None:
-        _need(positions, "positions", torch.int32, dev)
-        _need(inv_freq, "inv_freq", torch.float32, dev)
+        _check(positions, "positions", torch.int32, dev)
+        _check(inv_freq, "inv_freq", torch.float32, dev)
         if positions.shape != lead or inv_freq.dim() != 1:
             raise ValueError("positions must have the tokens' shape and inv_freq be [rot / 2]")
         rot = 2 * inv_freq.numel()
@@ -795,15 +838,15 @@ def qk_norm_rope(q, k, wq=None, wk=None, positions=None, inv_freq=None, norm: st
         if t is None:
             t = torch.empty(x.shape, dtype=out_dtype, device=dev)
         else:
-            _need(t, name, out_dtype, dev)
+            _check(t, name, out_dtype, dev)
             if t.shape != x.shape:
                 raise ValueError(f"{name} must have {name[0]}'s shape")
         outs.append(t)
-    with torch.cuda.device(dev):
-        rc = _lib.load().ckda_qk_norm_rope(
-            _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(outs[0]), _p(outs[1]),
-            n, Hq, Hk, d, rot, 1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype],
-            _DT[out_dtype], _stream_ptr(dev))
+    rc = _call(
+        _lib.load().ckda_qk_norm_rope, dev,
+        _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(outs[0]), _p(outs[1]),
+        n, Hq, Hk, d, rot, 1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype],
+        _DT[out_dtype])
     if rc != 0:
         raise CKDAError(rc, "ckda_qk_norm_rope")
     return outs[0], outs[1]
@@ -820,7 +863,7 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, inv
     n, Hq, Hk, d, rot, qs, ks = _qk_inputs(q, k, wq, wk, positions, inv_freq, norm)
     dev = q.device
     for name, t, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        _need(t, name, q.dtype, dev)
+        _check(t, name, q.dtype, dev)
         if t.shape != x.shape:
             raise ValueError(f"{name} must have {name[1]}'s shape")
     g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
@@ -834,13 +877,13 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, inv
             raise CKDAError(int(need), "ckda_qk_norm_rope_bwd_workspace_bytes")
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     if workspace is not None:
-        _need(workspace, "workspace", torch.uint8, dev)
-    with torch.cuda.device(dev):
-        rc = lib.ckda_qk_norm_rope_bwd(
-            _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(dq_out), _p(dk_out),
-            _p(g["dq"]), _p(g["dk"]), _p(g["dwq"]), _p(g["dwk"]), n, Hq, Hk, d, rot,
-            1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype], _p(workspace),
-            0 if workspace is None else workspace.numel(), _stream_ptr(dev))
+        _check(workspace, "workspace", torch.uint8, dev)
+    rc = _call(
+        lib.ckda_qk_norm_rope_bwd, dev,
+        _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(dq_out), _p(dk_out),
+        _p(g["dq"]), _p(g["dk"]), _p(g["dwq"]), _p(g["dwk"]), n, Hq, Hk, d, rot,
+        1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype], _p(workspace),
+        0 if workspace is None else workspace.numel())
     if rc != 0:
         raise CKDAError(rc, "ckda_qk_norm_rope_bwd")
     return g

@@ -274,9 +274,10 @@ int ckda_qk_norm_rope(const void* q, const void* k, const float* wq, const float
     for (int j = 0; j < 6; ++j)
       if (!(i == j && in_place[i]) && overlap(out[i], in[j])) return CKDA_ERR_INVALID_ARG;
   if (overlap(out[0], out[1])) return CKDA_ERR_INVALID_ARG;
-  const ckda::qkn::Args p{q, k, wq, wk, positions, inv_freq, q_out, k_out, nullptr, nullptr,
-                          nullptr, q_stride, k_stride, tokens, Hq, Hk, d, rot, interleaved, 0,
-                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps, 0};
+  const ckda::qkn::Args p{{{q, wq, q_out, nullptr, q_stride, Hq, 0, 0, 0},
+                           {k, wk, k_out, nullptr, k_stride, Hk, 0, 0, 0}},
+                          positions, inv_freq, nullptr, tokens, d, rot, interleaved,
+                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps};
   const cudaError_t err =
       ckda::launch_qk_norm_fwd(p, dtype, out_dtype, static_cast<cudaStream_t>(stream));
   return err == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
@@ -326,10 +327,11 @@ int ckda_qk_norm_rope_bwd(const void* q, const void* k, const float* wq, const f
   rc = check_workspace(workspace, workspace_bytes,
                        sums ? ckda::qk_norm_bwd_workspace_bytes(d) : 0, tens, 12);
   if (rc != CKDA_OK) return rc;
-  const ckda::qkn::Args p{q, k, wq, wk, positions, inv_freq, dq, dk, dq_out, dk_out,
-                          sums ? static_cast<float*>(workspace) : nullptr, q_stride, k_stride,
-                          tokens, Hq, Hk, d, rot, interleaved, 0,
-                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps, 0};
+  const ckda::qkn::Args p{{{q, wq, dq, dq_out, q_stride, Hq, 0, 0, 0},
+                           {k, wk, dk, dk_out, k_stride, Hk, 0, 0, 0}},
+                          positions, inv_freq, sums ? static_cast<float*>(workspace) : nullptr,
+                          tokens, d, rot, interleaved,
+                          norm == CKDA_NORM_RMS ? 1.f / (float)d : 1.f, eps};
   if (tokens == 0 && !sums) return CKDA_OK;
   const cudaError_t err =
       ckda::launch_qk_norm_bwd(p, dtype, dwq, dwk, static_cast<cudaStream_t>(stream));

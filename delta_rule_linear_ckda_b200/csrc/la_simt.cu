@@ -46,23 +46,32 @@ struct RecArgs {
   int* status;
 };
 
+template <int DK, int COLS>
+struct RecSmem {
+  float sq[kTile][DK], sk[kTile][DK], sv[kTile][COLS], sa[kTile];
+  float red[kTile][kRecThreads / COLS][COLS];
+};
+
 template <int DK, int COLS, typename Tin, typename Tout, bool REV>
-__global__ void __launch_bounds__(kRecThreads) la_rec_kernel(const RecArgs p) {
+__device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSmem<DK, COLS>& sm) {
   constexpr int RG = kRecThreads / COLS;  // row groups
   constexpr int RPT = DK / RG;            // rows per thread
   constexpr int LQ = kTile * DK / kRecThreads;
   constexpr int LV = kTile * COLS / kRecThreads;
   static_assert(RPT % 2 == 0 && LQ >= 1 && LV >= 1, "shape");
-  __shared__ __align__(16) float sq[kTile][DK], sk[kTile][DK];
-  __shared__ float sv[kTile][COLS], sa[kTile], red[kTile][RG][COLS];
+  auto& sq = sm.sq;
+  auto& sk = sm.sk;
+  auto& sv = sm.sv;
+  auto& sa = sm.sa;
+  auto& red = sm.red;
 
   const int tid = threadIdx.x;
   const int col = tid % COLS, g = tid / COLS;
   // block index: column slice, then head, then sequence (longest first)
   const int slices = p.DV / COLS;
-  const int j0 = (int)(blockIdx.x % slices) * COLS;
-  const int h = (int)(blockIdx.x / slices % p.H);
-  const int n = seq_longest_first(p.cu, p.n_seqs, (int)(blockIdx.x / slices / p.H));
+  const int j0 = (int)(block % slices) * COLS;
+  const int h = (int)(block / slices % p.H);
+  const int n = seq_longest_first(p.cu, p.n_seqs, (int)(block / slices / p.H));
   const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
   if (!sr.ok) return;
   const int len = (int)(sr.end - sr.begin);
@@ -137,21 +146,36 @@ __global__ void __launch_bounds__(kRecThreads) la_rec_kernel(const RecArgs p) {
     }
     // Backward in time the decay of token t acts behind its own term: it is
     // applied with token t - 1's, and the tile's first token's at the end.
-#pragma unroll 2
-    for (int tt = 0; tt < rows; ++tt) {
-      const int t = REV ? rows - 1 - tt : tt;
-      const float a = REV ? (tt == 0 ? 1.f : sa[t + 1]) : sa[t];
+    // Four tokens at a time, so that one's loads from shared memory and sums
+    // run under another's.
+    auto token = [&](int t, float a) {
       const float vv = sv[t][col];
       const float2 a2 = make_float2(a, a), v2 = make_float2(vv, vv);
-      float2 o = make_float2(0.f, 0.f);
+      float2 o = make_float2(0.f, 0.f), o1 = o;
 #pragma unroll
       for (int r = 0; r < RPT / 2; ++r) {
         const float2 k2 = *reinterpret_cast<const float2*>(&sk[t][i0 + 2 * r]);
         const float2 q2 = *reinterpret_cast<const float2*>(&sq[t][i0 + 2 * r]);
         X[r] = fma2(X[r], a2, mul2(k2, v2));
-        o = fma2(q2, X[r], o);
+        if (r & 1)
+          o1 = fma2(q2, X[r], o1);
+        else
+          o = fma2(q2, X[r], o);
       }
-      red[t][g][col] = o.x + o.y;
+      red[t][g][col] = (o.x + o1.x) + (o.y + o1.y);
+    };
+    if (rows == kTile) {
+#pragma unroll 4
+      for (int tt = 0; tt < kTile; ++tt) {
+        const int t = REV ? kTile - 1 - tt : tt;
+        token(t, REV ? (tt == 0 ? 1.f : sa[t + 1]) : sa[t]);
+      }
+    } else {
+#pragma unroll 1
+      for (int tt = 0; tt < rows; ++tt) {
+        const int t = REV ? rows - 1 - tt : tt;
+        token(t, REV ? (tt == 0 ? 1.f : sa[t + 1]) : sa[t]);
+      }
     }
     if (REV) {
       const float2 a2 = make_float2(sa[0], sa[0]);
@@ -181,6 +205,43 @@ __global__ void __launch_bounds__(kRecThreads) la_rec_kernel(const RecArgs p) {
       b[(size_t)(i0 + 2 * r + 1) * p.si] = X[r].y;
     }
   }
+}
+
+template <int DK, int COLS, typename Tin, typename Tout, bool REV>
+__global__ void __launch_bounds__(kRecThreads) la_rec_kernel(const RecArgs p) {
+  __shared__ __align__(16) RecSmem<DK, COLS> sm;
+  rec_body<DK, COLS, Tin, Tout, REV>(p, blockIdx.x, sm);
+}
+
+// The backward's three recurrences at once, when d_k = d_v: they do not depend
+// on one another, and a recurrence by itself leaves most SMs empty when there
+// are few heads.
+struct Rec3Args {
+  RecArgs fwd, rev[2];
+};
+
+template <int DK, int COLS, typename T>
+__global__ void __launch_bounds__(kRecThreads) la_rec3_kernel(const Rec3Args p) {
+  __shared__ __align__(16) RecSmem<DK, COLS> sm;
+  const unsigned which = blockIdx.x % 3, block = blockIdx.x / 3;
+  if (which == 0)
+    rec_body<DK, COLS, T, T, false>(p.fwd, block, sm);
+  else
+    rec_body<DK, COLS, T, T, true>(p.rev[which - 1], block, sm);
+}
+
+template <typename T>
+static cudaError_t rec3(int d, const Rec3Args& a, cudaStream_t st) {
+  const RecArgs& f = a.fwd;
+  const unsigned n = (unsigned)(f.DV / (f.DV == 16 ? 16 : 32)) * f.H * f.n_seqs;
+  switch (d) {
+    case 16: la_rec3_kernel<16, 16, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
+    case 32: la_rec3_kernel<32, 32, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
+    case 64: la_rec3_kernel<64, 32, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
+    case 128: la_rec3_kernel<128, 32, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
 }
 
 template <int DK, int COLS, typename Tin, typename Tout>
@@ -476,9 +537,16 @@ cudaError_t launch_la_bwd_simt(int dtype, int dk_, int dv_, const void* q, const
   const la::RecArgs av{k, q, dO, al, dSf, dS0, dv_, 1, dv, G, cu, n_seqs, T, H, dv_, status};
   const la::RecArgs ak{v, dO, q, al, dSf, nullptr, 1, dv_, dk, nullptr, cu, n_seqs, T, H, dk_,
                        status};
-  cudaError_t e = la::rec(dtype, dtype, dv_, aq, false, stream);
-  if (e == cudaSuccess) e = la::rec(dtype, dtype, dk_, av, true, stream);
-  if (e == cudaSuccess) e = la::rec(dtype, dtype, dv_, ak, true, stream);
+  cudaError_t e;
+  if (dk_ == dv_) {
+    const la::Rec3Args a{aq, {av, ak}};
+    e = dtype == CKDA_BF16 ? la::rec3<__nv_bfloat16>(dk_, a, stream)
+                           : la::rec3<float>(dk_, a, stream);
+  } else {
+    e = la::rec(dtype, dtype, dv_, aq, false, stream);
+    if (e == cudaSuccess) e = la::rec(dtype, dtype, dk_, av, true, stream);
+    if (e == cudaSuccess) e = la::rec(dtype, dtype, dv_, ak, true, stream);
+  }
   if (e != cudaSuccess) return e;
   if (slots > 0) {
     const la::DalphaArgs d{q, k, v, dO, al, St, G, part, cu, n_seqs, T, H, dk_, dv_, status};

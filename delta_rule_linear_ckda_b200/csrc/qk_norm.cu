@@ -13,10 +13,10 @@
 // thread owns two units of G adjacent channels (G = 8: 16 bytes of bf16) that
 // hold whole pairs, so that the turn needs no exchange between threads; the
 // d / (2 G) threads of a row are adjacent lanes and sum over it by shuffles.
-// A warp takes some heads of one token, queries' and keys' alike, so that a
+// A warp takes some of one token's query heads, or key heads, so that a
 // thread computes the sines and cosines of its own pairs once for all of them
-// and no barrier stands between the rows; the next rows are requested before
-// the present ones are used.
+// and no barrier stands between the rows.  It requests several rows per lane
+// at once (64 to 128 bytes) before it uses the first.
 //
 // Angles: the turns, position * inv_freq / (2 pi), and their reduction to
 // [-1/2, 1/2] are computed in 64 bits (error below 2^-50 of the turns), and
@@ -29,24 +29,40 @@ namespace qkn {
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 
+// G elements as they lie in memory.
 template <typename T, int G>
-__device__ __forceinline__ void load_unit(const T* p, float* x);
-template <>
-__device__ __forceinline__ void load_unit<float, 4>(const float* p, float* x) {
-  const float4 a = *reinterpret_cast<const float4*>(p);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-}
-template <>
-__device__ __forceinline__ void load_unit<float, 8>(const float* p, float* x) { load8_f32(p, x); }
-template <>
-__device__ __forceinline__ void load_unit<__nv_bfloat16, 4>(const __nv_bfloat16* p, float* x) {
-  const float4 a = load4_f32(p);
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-}
-template <>
-__device__ __forceinline__ void load_unit<__nv_bfloat16, 8>(const __nv_bfloat16* p, float* x) {
-  load8_f32(p, x);
-}
+struct Raw {
+  static constexpr int kWords = (int)sizeof(T) * G / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (kWords == 2) {
+      const uint2 v = *reinterpret_cast<const uint2*>(p);
+      w[0] = v.x; w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) {
+        const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(p) + i);
+        w[i] = v.x; w[i + 1] = v.y; w[i + 2] = v.z; w[i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = 0u;
+  }
+  __device__ __forceinline__ void get(float* x) const {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) {
+        x[2 * i] = __uint_as_float(w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < G; ++i) x[i] = __uint_as_float(w[i]);
+    }
+  }
+};
 
 template <typename T, int G>
 __device__ __forceinline__ void store_unit(T* p, const float* x) {
@@ -123,259 +139,272 @@ __device__ __forceinline__ void angles(const Args& p, int64_t t, int a, float2* 
   }
 }
 
-// A warp's rows: heads [h0, h1) of token t, RPW of them at a time.
+// A warp's rows: heads [h0, h1) of token t.
 struct Unit {
   int64_t t;
   int h0, h1;
 };
 
-__device__ __forceinline__ Unit unit_of(const Args& p, int64_t u) {
+__device__ __forceinline__ Unit unit_of(const Side& s, int64_t u) {
   Unit x;
-  const int groups = (p.Hq + p.Hk + p.heads_warp - 1) / p.heads_warp;
-  x.t = u / groups;
-  x.h0 = (int)(u - x.t * groups) * p.heads_warp;
-  x.h1 = min(p.Hq + p.Hk, x.h0 + p.heads_warp);
+  const int groups = (s.H + s.heads_warp - 1) / s.heads_warp;
+  x.t = groups == 1 ? u : u / groups;
+  x.h0 = (int)(u - x.t * groups) * s.heads_warp;
+  x.h1 = min(s.H, x.h0 + s.heads_warp);
   return x;
 }
 
 template <int G>
-struct Weights {
-  float q[2 * G], k[2 * G];
-  __device__ __forceinline__ void load(const Args& p, int a, int b) {
+__device__ __forceinline__ void load_w(const float* p, int a, int b, float* w) {
 #pragma unroll
-    for (int i = 0; i < 2 * G; ++i) {
-      const int ch = i < G ? a + i : b + i - G;
-      q[i] = p.wq != nullptr ? __ldg(p.wq + ch) : 1.f;
-      k[i] = p.wk != nullptr ? __ldg(p.wk + ch) : 1.f;
-    }
-  }
-};
-
-template <typename T, int D>
-__device__ __forceinline__ const T* row_in(const Args& p, int64_t t, int hh) {
-  return hh < p.Hq ? static_cast<const T*>(p.q) + t * p.q_stride + (int64_t)hh * D
-                   : static_cast<const T*>(p.k) + t * p.k_stride + (int64_t)(hh - p.Hq) * D;
+  for (int i = 0; i < 2 * G; ++i) w[i] = p != nullptr ? __ldg(p + (i < G ? a + i : b + i - G)) : 1.f;
 }
 
-// A row's offset in a contiguous [tokens, heads, D] tensor of its own.
-template <int D>
-__device__ __forceinline__ int64_t row_at(const Args& p, int64_t t, int hh) {
-  return hh < p.Hq ? (t * p.Hq + hh) * D : (t * p.Hk + hh - p.Hq) * D;
-}
+// Rows that a lane requests at once.
+template <typename T, bool BWD>
+constexpr int kBatch = (sizeof(T) == 2 ? 4 : 2) / (BWD ? 2 : 1);
 
 template <typename Tin, typename Tout, int D, int G>
 __global__ void __launch_bounds__(kThreads) fwd_kernel(const Args p) {
   constexpr int TPR = D / (2 * G);  // threads per row
   constexpr int RPW = 32 / TPR;     // rows per warp and pass
+  constexpr int NB = kBatch<Tin, false>;
   const int lane = threadIdx.x & 31;
   const int c = lane % TPR, rg = lane / TPR;
-  const int64_t u = (int64_t)blockIdx.x * kWarps + (threadIdx.x >> 5);
-  if (u >= p.units) return;
-  const Unit un = unit_of(p, u);
+  const bool keys = blockIdx.x >= p.s[0].ctas;
+  const Side& sd = keys ? p.s[1] : p.s[0];
+  const int64_t u =
+      (int64_t)(blockIdx.x - (keys ? p.s[0].ctas : 0u)) * kWarps + (threadIdx.x >> 5);
+  if (u >= sd.units) return;
+  const Unit un = unit_of(sd, u);
   int a, b;
   bool trn;
   units<G>(c, p.rot, p.interleaved, &a, &b, &trn);
-  float x[G], y[G];
-  auto fetch = [&](int hh) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) x[i] = y[i] = 0.f;
-    if (hh < un.h1) {
-      const Tin* src = row_in<Tin, D>(p, un.t, hh);
-      load_unit<Tin, G>(src + a, x);
-      load_unit<Tin, G>(src + b, y);
-    }
-  };
-  fetch(un.h0 + rg);
-  Weights<G> w;
-  w.load(p, a, b);
+  const Tin* src = static_cast<const Tin*>(sd.x) + un.t * sd.stride;
+  Tout* dst = static_cast<Tout*>(sd.out) + un.t * sd.H * D;
+  Raw<Tin, G> ra[NB], rb[NB];
+  float w[2 * G];
   float2 cs[G];
-  if (trn) angles<G>(p, un.t, a, cs);
   // (every lane takes the same trips, so the shuffles meet)
-  for (int r0 = un.h0; r0 < un.h1; r0 += RPW) {
-    const int hh = r0 + rg;
-    const bool isq = hh < p.Hq;
-    float u0[G], v0[G];
+  for (int r0 = un.h0; r0 < un.h1; r0 += RPW * NB) {
 #pragma unroll
-    for (int i = 0; i < G; ++i) {
-      u0[i] = x[i];
-      v0[i] = y[i];
+    for (int n = 0; n < NB; ++n) {
+      const int hh = r0 + n * RPW + rg;
+      if (hh < un.h1) {
+        ra[n].load(src + (int64_t)hh * D + a);
+        rb[n].load(src + (int64_t)hh * D + b);
+      } else {
+        ra[n].zero();
+        rb[n].zero();
+      }
     }
-    fetch(hh + RPW);
-    float ss = 0.f;
-#pragma unroll
-    for (int i = 0; i < G; ++i) ss = fmaf(u0[i], u0[i], fmaf(v0[i], v0[i], ss));
-#pragma unroll
-    for (int o = TPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float r = inv_norm(ss, p);
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      u0[i] *= r * (isq ? w.q[i] : w.k[i]);
-      v0[i] *= r * (isq ? w.q[G + i] : w.k[G + i]);
+    if (r0 == un.h0) {
+      load_w<G>(sd.w, a, b, w);
+      if (trn) angles<G>(p, un.t, a, cs);
     }
-    if (trn) turn<G>(u0, v0, cs, p.interleaved, 1.f);
-    if (hh < un.h1) {
-      Tout* dst = static_cast<Tout*>(isq ? p.oq : p.ok) + row_at<D>(p, un.t, hh);
-      store_unit<Tout, G>(dst + a, u0);
-      store_unit<Tout, G>(dst + b, v0);
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+      if (r0 + n * RPW >= un.h1) break;
+      const int hh = r0 + n * RPW + rg;
+      float x[G], y[G];
+      ra[n].get(x);
+      rb[n].get(y);
+      float ss = 0.f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+#pragma unroll
+      for (int o = TPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      const float r = inv_norm(ss, p);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        x[i] *= r * w[i];
+        y[i] *= r * w[G + i];
+      }
+      if (trn) turn<G>(x, y, cs, p.interleaved, 1.f);
+      if (hh < un.h1) {
+        store_unit<Tout, G>(dst + (int64_t)hh * D + a, x);
+        store_unit<Tout, G>(dst + (int64_t)hh * D + b, y);
+      }
     }
   }
 }
 
-// The warps walk the units with a stride of the grid, so that each adds its
-// rows' shares of dw up in registers and a CTA leaves one partial sum per
-// weight; dw_kernel adds those in a fixed order.
+// The warps walk the units of their side with a stride of its CTAs, so that
+// each adds its rows' shares of dw up in registers and a CTA leaves one
+// partial sum per channel; dw_kernel adds those in a fixed order.
 template <typename T, int D, int G, bool SUMS>
 __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
   constexpr int TPR = D / (2 * G);
   constexpr int RPW = 32 / TPR;
-  __shared__ float sw[2][kWarps][D];
+  constexpr int NB = kBatch<T, true>;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = lane % TPR, rg = lane / TPR;
+  const bool keys = blockIdx.x >= p.s[0].ctas;
+  const Side& sd = keys ? p.s[1] : p.s[0];
+  const unsigned cta = blockIdx.x - (keys ? p.s[0].ctas : 0u);
   int a, b;
   bool trn;
   units<G>(c, p.rot, p.interleaved, &a, &b, &trn);
-  Weights<G> w;
-  w.load(p, a, b);
-  float dwq[2 * G], dwk[2 * G];
+  float w[2 * G], dw[SUMS ? 2 * G : 1];
+  load_w<G>(sd.w, a, b, w);
+  if constexpr (SUMS) {
 #pragma unroll
-  for (int i = 0; i < 2 * G; ++i) dwq[i] = dwk[i] = 0.f;
-  for (int64_t uu = (int64_t)blockIdx.x * kWarps + warp; uu < p.units;
-       uu += (int64_t)gridDim.x * kWarps) {
-    const Unit un = unit_of(p, uu);
+    for (int i = 0; i < 2 * G; ++i) dw[i] = 0.f;
+  }
+  for (int64_t uu = (int64_t)cta * kWarps + warp; uu < sd.units;
+       uu += (int64_t)sd.ctas * kWarps) {
+    const Unit un = unit_of(sd, uu);
+    const T* src = static_cast<const T*>(sd.x) + un.t * sd.stride;
+    const T* gr = static_cast<const T*>(sd.g) + un.t * sd.H * D;
+    T* dst = static_cast<T*>(sd.out) + un.t * sd.H * D;
+    Raw<T, G> ra[NB], rb[NB], ga[NB], gb[NB];
     float2 cs[G];
-    if (trn) angles<G>(p, un.t, a, cs);
-    for (int r0 = un.h0; r0 < un.h1; r0 += RPW) {
-      const int hh = r0 + rg;
-      const bool ok = hh < un.h1, isq = hh < p.Hq;
-      float x[G], y[G], u[G], v[G];
+    for (int r0 = un.h0; r0 < un.h1; r0 += RPW * NB) {
 #pragma unroll
-      for (int i = 0; i < G; ++i) x[i] = y[i] = u[i] = v[i] = 0.f;
-      const int64_t at = row_at<D>(p, un.t, hh);
-      if (ok) {
-        const T* src = row_in<T, D>(p, un.t, hh);
-        const T* gr = static_cast<const T*>(isq ? p.gq : p.gk) + at;
-        load_unit<T, G>(src + a, x);
-        load_unit<T, G>(src + b, y);
-        load_unit<T, G>(gr + a, u);
-        load_unit<T, G>(gr + b, v);
-      }
-      if (trn) turn<G>(u, v, cs, p.interleaved, -1.f);
-      float ss = 0.f, dot = 0.f;
-#pragma unroll
-      for (int i = 0; i < G; ++i) ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
-#pragma unroll
-      for (int i = 0; i < G; ++i) {
-        dot = fmaf(x[i] * u[i], isq ? w.q[i] : w.k[i], dot);
-        dot = fmaf(y[i] * v[i], isq ? w.q[G + i] : w.k[G + i], dot);
-      }
-#pragma unroll
-      for (int o = TPR / 2; o >= 1; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        dot += __shfl_xor_sync(0xffffffffu, dot, o);
-      }
-      const float r = inv_norm(ss, p);
-      const float m = p.c * r * r * r * dot;
-      if (SUMS) {  // (a lane without a row adds zeros)
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          const float e = u[i] * (x[i] * r), f = v[i] * (y[i] * r);
-          dwq[i] += isq ? e : 0.f;
-          dwq[G + i] += isq ? f : 0.f;
-          dwk[i] += isq ? 0.f : e;
-          dwk[G + i] += isq ? 0.f : f;
+      for (int n = 0; n < NB; ++n) {
+        const int hh = r0 + n * RPW + rg;
+        if (hh < un.h1) {
+          ra[n].load(src + (int64_t)hh * D + a);
+          rb[n].load(src + (int64_t)hh * D + b);
+          ga[n].load(gr + (int64_t)hh * D + a);
+          gb[n].load(gr + (int64_t)hh * D + b);
+        } else {
+          ra[n].zero();
+          rb[n].zero();
+          ga[n].zero();
+          gb[n].zero();
         }
       }
+      if (trn && r0 == un.h0) angles<G>(p, un.t, a, cs);
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        u[i] = fmaf(r * (isq ? w.q[i] : w.k[i]), u[i], -m * x[i]);
-        v[i] = fmaf(r * (isq ? w.q[G + i] : w.k[G + i]), v[i], -m * y[i]);
-      }
-      if (ok) {
-        T* dst = static_cast<T*>(isq ? p.oq : p.ok) + at;
-        store_unit<T, G>(dst + a, u);
-        store_unit<T, G>(dst + b, v);
+      for (int n = 0; n < NB; ++n) {
+        if (r0 + n * RPW >= un.h1) break;
+        const int hh = r0 + n * RPW + rg;
+        float x[G], y[G], u[G], v[G];
+        ra[n].get(x);
+        rb[n].get(y);
+        ga[n].get(u);
+        gb[n].get(v);
+        if (trn) turn<G>(u, v, cs, p.interleaved, -1.f);
+        float ss = 0.f, dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          ss = fmaf(x[i], x[i], fmaf(y[i], y[i], ss));
+          dot = fmaf(x[i] * u[i], w[i], dot);
+          dot = fmaf(y[i] * v[i], w[G + i], dot);
+        }
+#pragma unroll
+        for (int o = TPR / 2; o >= 1; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          dot += __shfl_xor_sync(0xffffffffu, dot, o);
+        }
+        const float r = inv_norm(ss, p);
+        const float m = p.c * r * r * r * dot;
+        if constexpr (SUMS) {  // (a lane without a row adds zeros)
+#pragma unroll
+          for (int i = 0; i < G; ++i) {
+            dw[i] = fmaf(u[i], x[i] * r, dw[i]);
+            dw[G + i] = fmaf(v[i], y[i] * r, dw[G + i]);
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          u[i] = fmaf(r * w[i], u[i], -m * x[i]);
+          v[i] = fmaf(r * w[G + i], v[i], -m * y[i]);
+        }
+        if (hh < un.h1) {
+          store_unit<T, G>(dst + (int64_t)hh * D + a, u);
+          store_unit<T, G>(dst + (int64_t)hh * D + b, v);
+        }
       }
     }
   }
   if constexpr (SUMS) {
+    __shared__ float sw[kWarps][D];
     // lanes c, c + TPR, ... of a warp hold the same channels
 #pragma unroll
     for (int i = 0; i < 2 * G; ++i) {
 #pragma unroll
-      for (int o = TPR; o < 32; o <<= 1) {
-        dwq[i] += __shfl_xor_sync(0xffffffffu, dwq[i], o);
-        dwk[i] += __shfl_xor_sync(0xffffffffu, dwk[i], o);
-      }
-      const int ch = i < G ? a + i : b + i - G;
-      if (lane < TPR) {
-        sw[0][warp][ch] = dwq[i];
-        sw[1][warp][ch] = dwk[i];
-      }
+      for (int o = TPR; o < 32; o <<= 1) dw[i] += __shfl_xor_sync(0xffffffffu, dw[i], o);
+      if (lane < TPR) sw[warp][i < G ? a + i : b + i - G] = dw[i];
     }
     __syncthreads();
-    for (int e = threadIdx.x; e < 2 * D; e += kThreads) {
-      const int which = e / D, ch = e - which * D;
+    for (int ch = threadIdx.x; ch < D; ch += kThreads) {
       float s = 0.f;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) s += sw[which][k][ch];
-      p.part[((size_t)blockIdx.x * 2 + which) * D + ch] = s;
+      for (int k = 0; k < kWarps; ++k) s += sw[k][ch];
+      p.part[(size_t)blockIdx.x * D + ch] = s;
     }
   }
 }
 
-// dw[ch] = the sum of `n` partial sums: a CTA per 32 channels of one weight,
-// 64-bit sums in a fixed order.
-__global__ void __launch_bounds__(256) dw_kernel(const float* __restrict__ part, int n, int d,
-                                                 float* __restrict__ dwq, float* __restrict__ dwk) {
-  __shared__ double red[8][32];
+// dw[ch] = the sum of the CTAs' partial sums: a CTA per 32 channels of one
+// weight, 64-bit sums in a fixed order.  A warp has four partial sums on
+// their way at a time: with one, the chain of loads took 26 us for 444 CTAs.
+__global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part, int nq, int nk,
+                                                  int d, float* __restrict__ dwq,
+                                                  float* __restrict__ dwk) {
+  __shared__ double red[32][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int ch = blockIdx.x * 32 + lane;
+  const int i0 = blockIdx.y ? nq : 0, i1 = blockIdx.y ? nq + nk : nq;
+  float* o = blockIdx.y ? dwk : dwq;
+  if (o == nullptr) return;
   double s = 0.0;
-  if (ch < d)
-    for (int i = w; i < n; i += 8) s += (double)part[((size_t)i * 2 + blockIdx.y) * d + ch];
+  if (ch < d) {
+    for (int i = i0 + w; i < i1; i += 128) {
+      float x[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        x[e] = i + 32 * e < i1 ? __ldg(part + (size_t)(i + 32 * e) * d + ch) : 0.f;
+      s += ((double)x[0] + (double)x[1]) + ((double)x[2] + (double)x[3]);
+    }
+  }
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && ch < d) {
 #pragma unroll
-    for (int i = 1; i < 8; ++i) s += red[i][lane];
-    float* o = blockIdx.y ? dwk : dwq;
-    if (o != nullptr) o[ch] = (float)s;
+    for (int i = 1; i < 32; ++i) s += red[i][lane];
+    o[ch] = (float)s;
   }
 }
 
-constexpr int kBwdGrid = 148 * 4;
+constexpr int kBwdCtas = 148 * 3;  // per side at most, with sums: as many as an SM holds twice
 
-// Heads of a token that one warp takes: all of them (in up to 8 passes) when
-// the tokens alone give every SM 16 warps, else one pass's.
-static void plan(Args* p, int rpw) {
-  const int heads = p->Hq + p->Hk;
-  const int64_t all = p->tokens * ((heads + 8 * rpw - 1) / (8 * rpw));
-  p->heads_warp = all >= 148 * 16 ? 8 * rpw : rpw;
-  p->units = p->tokens * ((heads + p->heads_warp - 1) / p->heads_warp);
+// Heads of a token that one warp takes: all of them (in up to `most` passes)
+// when the tokens alone give every SM 16 warps, else one pass's.
+static void plan(Args* p, int rpw, int most, unsigned cap) {
+  for (Side& s : p->s) {
+    const int64_t all = p->tokens * ((s.H + most * rpw - 1) / (most * rpw));
+    s.heads_warp = all >= 148 * 16 ? most * rpw : rpw;
+    s.units = p->tokens * ((s.H + s.heads_warp - 1) / s.heads_warp);
+    const int64_t ctas = (s.units + kWarps - 1) / kWarps;
+    s.ctas = cap != 0 && ctas > cap ? cap : (unsigned)ctas;
+  }
 }
 
 template <typename Tin, typename Tout, int D, int G>
 static cudaError_t launch_fwd(Args p, cudaStream_t st) {
-  plan(&p, 32 / (D / (2 * G)));
-  fwd_kernel<Tin, Tout, D, G><<<(unsigned)((p.units + kWarps - 1) / kWarps), kThreads, 0, st>>>(p);
+  plan(&p, 32 / (D / (2 * G)), 8, 0);
+  fwd_kernel<Tin, Tout, D, G><<<p.s[0].ctas + p.s[1].ctas, kThreads, 0, st>>>(p);
   return cudaGetLastError();
 }
 
 template <typename T, int D, int G>
 static cudaError_t launch_bwd(Args p, float* dwq, float* dwk, cudaStream_t st) {
-  plan(&p, 32 / (D / (2 * G)));
-  const int64_t ctas = (p.units + kWarps - 1) / kWarps;
-  const int grid = (int)(ctas < kBwdGrid ? ctas : kBwdGrid);  // 0 without tokens: dw = 0
+  plan(&p, 32 / (D / (2 * G)), 8, p.part != nullptr ? kBwdCtas : 0);
+  const unsigned grid = p.s[0].ctas + p.s[1].ctas;  // 0 without tokens: dw = 0
   cudaError_t e = cudaSuccess;
   if (grid > 0) {
     if (p.part != nullptr)
       bwd_kernel<T, D, G, true><<<grid, kThreads, 0, st>>>(p);
     else
-      bwd_kernel<T, D, G, false><<<(unsigned)ctas, kThreads, 0, st>>>(p);
+      bwd_kernel<T, D, G, false><<<grid, kThreads, 0, st>>>(p);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && p.part != nullptr) {
-    dw_kernel<<<dim3((D + 31) / 32, 2), 256, 0, st>>>(p.part, grid, D, dwq, dwk);
+    dw_kernel<<<dim3((D + 31) / 32, 2), 1024, 0, st>>>(p.part, (int)p.s[0].ctas, (int)p.s[1].ctas, D,
+                                                      dwq, dwk);
     e = cudaGetLastError();
   }
   return e;
@@ -430,6 +459,6 @@ cudaError_t launch_qk_norm_bwd(const qkn::Args& p, int dtype, float* dwq, float*
                             : qkn::bwd_d<float>(p, dwq, dwk, st);
 }
 
-size_t qk_norm_bwd_workspace_bytes(int d) { return (size_t)qkn::kBwdGrid * 2 * d * 4; }
+size_t qk_norm_bwd_workspace_bytes(int d) { return (size_t)qkn::kBwdCtas * 2 * d * 4; }
 
 }  // namespace ckda

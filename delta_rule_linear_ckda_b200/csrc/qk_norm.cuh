@@ -6,20 +6,28 @@
 namespace ckda {
 namespace qkn {
 
+// The queries (0) or the keys (1).
+struct Side {
+  const void* x;      // row of token t and head h at x + t * stride + h * d
+  const float* w;     // [d] or NULL (ones)
+  void* out;          // forward: z; backward: dx; [tokens, H, d]
+  const void* g;      // backward: dz [tokens, H, d]
+  int64_t stride;
+  int H;
+  // set at launch
+  int heads_warp;     // heads of a token that one warp takes
+  int64_t units;      // warps' shares
+  unsigned ctas;      // of the grid, the queries' first
+};
+
 struct Args {
-  const void *q, *k;      // rows of token t at q + t * q_stride + head * d
-  const float *wq, *wk;   // [d] or NULL (ones)
+  Side s[2];
   const int32_t* pos;     // [tokens]
   const float* inv_freq;  // [rot / 2]
-  void *oq, *ok;          // forward: z; backward: dx; [tokens, heads, d]
-  const void *gq, *gk;    // backward: dz [tokens, heads, d]
-  float* part;            // backward: [gridDim.x][2][d] sums of dw, or NULL
-  int64_t q_stride, k_stride;
+  float* part;            // backward: [ctas][d] sums of dw, or NULL
   int64_t tokens;
-  int Hq, Hk, d, rot, interleaved;
-  int heads_warp;         // heads of a token that one warp takes (set at launch, as units)
+  int d, rot, interleaved;
   float c, eps;
-  int64_t units;          // warps' shares
 };
 
 }  // namespace qkn
