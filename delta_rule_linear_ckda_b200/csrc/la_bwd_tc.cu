@@ -371,6 +371,19 @@ struct Args {
   int* status;
 };
 
+// 16 bytes, requested where this stands (a plain load may be moved down to its
+// use).
+__device__ __forceinline__ void ld4(const float* p, float* x) {
+  asm volatile("ld.global.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+               : "l"(p));
+}
+
+// Pulls `bytes` (a multiple of 16) into L2.
+__device__ __forceinline__ void prefetch_l2_bulk(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // V_t = c_t V_{t-1} + b_t over 128 positions, four per lane; V_{-1} = 0.
 __device__ __forceinline__ void lin_scan(const float* c, const float* b, float* v, int lane) {
   float A = c[0], B = b[0];
@@ -507,6 +520,15 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if ((len = decode(u, &t0, &h)) > 0) break;
   if (u < p.units && mma_warp && lane == 0) load(t0, h);
   if (u < p.units) loaded = true;
+  // this thread's row and columns of S, then of G: what is left of it to split
+  float X[DV / 2];
+  const size_t mine = (size_t)(DV / 2 * hf) * DK + 4 * i;
+  auto states = [&](const float* kept, int64_t w) {
+    const float* a = kept + w * state_floats(DV) + mine;
+#pragma unroll
+    for (int e = 0; e < DV / 2; e += 4) ld4(a + (size_t)e * DK, X + e);
+  };
+  if (!mma_warp && u < p.units) states(p.Sk, u);
   uint32_t ph = 0, g3 = 0;
 #pragma unroll 1
   while (u < p.units) {
@@ -516,11 +538,6 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     for (; un < p.units; un += gridDim.x)
       if ((lenn = decode(un, &t0n, &hn)) > 0) break;
 
-    float X[DV / 2];  // a row of S, later of G: what is left of it to split
-    const float4* Sg = reinterpret_cast<const float4*>(p.Sk + u * state_floats(DV)) +
-                       (size_t)(DV / 8 * hf) * DK + i;
-    const float4* Gg = reinterpret_cast<const float4*>(p.Gk + u * state_floats(DV)) +
-                       (size_t)(DV / 8 * hf) * DK + i;
     // one bf16 term of X into a tile, X keeps the rest
     auto term = [&](uint32_t off) {
 #pragma unroll
@@ -538,14 +555,18 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     };
     float z = 0.f;
     if (!mma_warp) {
+      const float* g = p.Gk + u * state_floats(DV) + mine;
+      float y[DV / 2];  // all on their way at once
 #pragma unroll
-      for (int e = 0; e < DV / 8; ++e) {
-        const float4 x = __ldcs(Sg + (size_t)e * DK), y = __ldg(Gg + (size_t)e * DK);
-        X[4 * e] = x.x; X[4 * e + 1] = x.y; X[4 * e + 2] = x.z; X[4 * e + 3] = x.w;
-        z = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, z))));
-      }
+      for (int e = 0; e < DV / 2; e += 4) ld4(g + (size_t)e * DK, y + e);
+#pragma unroll
+      for (int e = 0; e < DV / 2; ++e) z = fmaf(X[e], y[e], z);
 #pragma unroll
       for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    }
+    if (mma_warp && lane == 0 && un < p.units) {
+      prefetch_l2_bulk(p.Sk + un * state_floats(DV), state_floats(DV) * 4);
+      prefetch_l2_bulk(p.Gk + un * state_floats(DV), state_floats(DV) * 4);
     }
     // the last unit's gradients have left their tiles
     if (mma_warp && lane == 0) bulk_wait_read_all();
@@ -620,11 +641,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       }
       // G's rows on their way while the products run
       if (ok) {
-#pragma unroll
-        for (int e = 0; e < DV / 8; ++e) {
-          const float4 y = __ldcs(Gg + (size_t)e * DK);
-          X[4 * e] = y.x; X[4 * e + 1] = y.y; X[4 * e + 2] = y.z; X[4 * e + 3] = y.w;
-        }
+        states(p.Gk, u);
         ok = wait(B_SC, ph) && wait(B_DS, ph);
         tc_fence_after();
       }
@@ -639,18 +656,19 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       term(OFF_T);
       fence_proxy_async_smem();
       const bool in = i < len;
+      // the decays between block J and this row's
+      auto between = [&](int J) -> float {
+        return (w4 > 1 && J < 1 ? tot.y : 1.f) * (w4 > 2 && J < 2 ? tot.z : 1.f);
+      };
       if (hf == 0) {
         // R(t) = sum_{j < t} D(t - 1, j) W_ij runs along the row; column t of
         // the block then sums D(i, t) R(t) over its rows
         float R = 0.f;
 #pragma unroll 1
         for (int J = 0; J <= w4; ++J) {
-          float d = pw;  // decays between block J and this row's
-          if (w4 > 1 && J < 1) d *= tot.y;
-          if (w4 > 2 && J < 2) d *= tot.z;
-          // D(i, t) in the diagonal block, from t = i down
           float dd[32];
           if (J == w4) {
+            // D(i, t) in the diagonal block, from t = i down
             float run = 1.f;
             const float a = F[F_A + i];
 #pragma unroll
@@ -660,21 +678,41 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
               run = t <= lane ? run * at : run;
             }
           } else {
+            const float d = pw * between(J);
 #pragma unroll
-            for (int t = 0; t < 32; ++t) dd[t] = d * F[F_SW + 32 * J + t];
+            for (int t = 0; t < 32; t += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(F + F_SW + 32 * J + t);
+              dd[t] = d * f.x; dd[t + 1] = d * f.y; dd[t + 2] = d * f.z; dd[t + 3] = d * f.w;
+            }
           }
 #pragma unroll
-          for (int e = 0; e < 32; e += 16) {
-            float s1[16], s2[16];
-            tmem_ld16(row + TM_S1 + 32 * J + e, s1);
-            tmem_ld16(row + TM_S2 + 32 * J + e, s2);
+          for (int e = 0; e < 32; e += 8) {
+            float s1[8], s2[8];
+            tmem_ld8(row + TM_S1 + 32 * J + e, s1);
+            tmem_ld8(row + TM_S2 + 32 * J + e, s2);
             tmem_ld_wait();
+            if (J == w4 || len < C) {
+              const int last = in ? (J == w4 ? lane : 31) : -1;
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-              const bool on = in && (J < w4 || e + t <= lane);
-              const float w = on ? s1[t] * s2[t] : 0.f;
-              dd[e + t] = on ? dd[e + t] * R : 0.f;
-              R = fmaf(F[F_A + 32 * J + e + t], R, w);
+              for (int t = 0; t < 8; ++t) {
+                s1[t] = e + t <= last ? s1[t] * s2[t] : 0.f;
+                dd[e + t] = e + t <= last ? dd[e + t] : 0.f;
+              }
+            } else {
+#pragma unroll
+              for (int t = 0; t < 8; ++t) s1[t] *= s2[t];
+            }
+#pragma unroll
+            for (int t = 0; t < 8; t += 4) {
+              const float4 f = *reinterpret_cast<const float4*>(F + F_A + 32 * J + e + t);
+              dd[e + t] *= R;
+              R = fmaf(f.x, R, s1[t]);
+              dd[e + t + 1] *= R;
+              R = fmaf(f.y, R, s1[t + 1]);
+              dd[e + t + 2] *= R;
+              R = fmaf(f.z, R, s1[t + 2]);
+              dd[e + t + 3] *= R;
+              R = fmaf(f.w, R, s1[t + 3]);
             }
           }
           // lane t gets the sum of dd[t] over the lanes
@@ -697,41 +735,47 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       } else {
 #pragma unroll 1
         for (int J = 0; J < 4; ++J) {
-          float s1[32], s2[32];
-          if (J <= w4) {
-            tmem_ld32(row + TM_S1 + 32 * J, s1);
-            tmem_ld32(row + TM_S2 + 32 * J, s2);
-            tmem_ld_wait();
+          const float d = J < w4 ? pw * between(J) : 0.f;
+          float run = in ? 1.f : 0.f;
+          const float a = F[F_A + i];
+#pragma unroll 1
+          for (int e = 16; e >= 0; e -= 16) {
+            float s1[16], s2[16];
+            if (J <= w4) {
+              tmem_ld16(row + TM_S1 + 32 * J + e, s1);
+              tmem_ld16(row + TM_S2 + 32 * J + e, s2);
+              tmem_ld_wait();
+            }
             if (J == w4) {
-              float run = 1.f;
-              const float a = F[F_A + i];
 #pragma unroll
-              for (int t = 31; t >= 0; --t) {
-                const float at = __shfl_sync(0xffffffffu, a, t);
-                const bool on = in && t <= lane;
+              for (int t = 15; t >= 0; --t) {
+                const float at = __shfl_sync(0xffffffffu, a, e + t);
+                const bool on = e + t <= lane;
                 s1[t] = on ? s1[t] * run : 0.f;
                 s2[t] = on ? s2[t] * run : 0.f;
-                run = t <= lane ? run * at : run;
+                run = on ? run * at : run;
               }
-            } else {
-              float d = pw;
-              if (w4 > 1 && J < 1) d *= tot.y;
-              if (w4 > 2 && J < 2) d *= tot.z;
+            } else if (J < w4) {
+              const float2 d2 = make_float2(d, d);
 #pragma unroll
-              for (int t = 0; t < 32; ++t) {
-                const float f = d * F[F_SW + 32 * J + t];
-                s1[t] = in ? s1[t] * f : 0.f;
-                s2[t] = in ? s2[t] * f : 0.f;
+              for (int t = 0; t < 16; t += 2) {
+                const float2 f = mul2(d2, *reinterpret_cast<const float2*>(F + F_SW + 32 * J + e + t));
+                const float2 x = mul2(make_float2(s1[t], s1[t + 1]), f);
+                const float2 y = mul2(make_float2(s2[t], s2[t + 1]), f);
+                s1[t] = x.x; s1[t + 1] = x.y;
+                s2[t] = y.x; s2[t + 1] = y.y;
               }
             }
-          } else {
+            if (J > w4 || !in) {
 #pragma unroll
-            for (int t = 0; t < 32; ++t) s1[t] = s2[t] = 0.f;
-          }
+              for (int t = 0; t < 16; ++t) s1[t] = s2[t] = 0.f;
+            }
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            *reinterpret_cast<uint4*>(sm + OFF_P + sw128_chunk(i, 32 * J + e, 128)) = pack8(s1 + e);
-            *reinterpret_cast<uint4*>(sm + OFF_E + sw128_chunk(i, 32 * J + e, 128)) = pack8(s2 + e);
+            for (int t = 0; t < 16; t += 8) {
+              const uint32_t o = sw128_chunk(i, 32 * J + e + t, 128);
+              *reinterpret_cast<uint4*>(sm + OFF_P + o) = pack8(s1 + t);
+              *reinterpret_cast<uint4*>(sm + OFF_E + o) = pack8(s2 + t);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -796,6 +840,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       ok = wait(B_G, g3 + 1);
       term(OFF_T);
       fence_proxy_async_smem();
+      if (un < p.units) states(p.Sk, un);  // in registers until the next unit
     }
     ok = __syncthreads_and(ok);
     if (!ok) break;
