@@ -358,7 +358,7 @@ constexpr uint32_t TM_S1 = 0, TM_S2 = 128;           // Q K^T, dO V^T
 constexpr uint32_t TM_DV = 0, TM_DK = 128, TM_DQ = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kCompute = 256;
-constexpr int kThreads = kCompute + 32;
+constexpr int kThreads = kCompute;  // more warps would leave a thread less than 255 registers
 
 struct Args {
   Decay al;
@@ -498,7 +498,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
   };
 
-  const bool mma_warp = warp == 8;
+  const bool lead = warp == 0;  // this warp also issues the products, loads and stores
   const uint64_t q_k = smem_desc(sb + OFF_Q, 16, 1024, kSwizzle128);      // K-major
   const uint64_t q_m = smem_desc(sb + OFF_Q, 16384, 1024, kSwizzle128);   // MN-major
   constexpr uint64_t kTile = 32768 >> 4;
@@ -518,17 +518,20 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   int len = 0;
   for (; u < p.units; u += gridDim.x)
     if ((len = decode(u, &t0, &h)) > 0) break;
-  if (u < p.units && mma_warp && lane == 0) load(t0, h);
+  if (u < p.units && lead && lane == 0) load(t0, h);
   if (u < p.units) loaded = true;
-  // this thread's row and columns of S, then of G: what is left of it to split
-  float X[DV / 2];
+  // this thread's row and columns of S and of G: what is left of them to split
+  float S[DV / 2], G[DV / 2];
   const size_t mine = (size_t)(DV / 2 * hf) * DK + 4 * i;
-  auto states = [&](const float* kept, int64_t w) {
+  auto states = [&](float (&X)[DV / 2], const float* kept, int64_t w) {
     const float* a = kept + w * state_floats(DV) + mine;
 #pragma unroll
     for (int e = 0; e < DV / 2; e += 4) ld4(a + (size_t)e * DK, X + e);
   };
-  if (!mma_warp && u < p.units) states(p.Sk, u);
+  if (u < p.units) {
+    states(S, p.Sk, u);
+    states(G, p.Gk, u);
+  }
   uint32_t ph = 0, g3 = 0;
 #pragma unroll 1
   while (u < p.units) {
@@ -539,7 +542,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       if ((lenn = decode(un, &t0n, &hn)) > 0) break;
 
     // one bf16 term of X into a tile, X keeps the rest
-    auto term = [&](uint32_t off) {
+    auto term = [&](uint32_t off, float (&X)[DV / 2]) {
 #pragma unroll
       for (int e = 0; e < DV / 2; e += 8) {
         uint32_t w[4];
@@ -554,38 +557,17 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       }
     };
     float z = 0.f;
-    if (!mma_warp) {
-      const float* g = p.Gk + u * state_floats(DV) + mine;
-      float y[DV / 2];  // all on their way at once
 #pragma unroll
-      for (int e = 0; e < DV / 2; e += 4) ld4(g + (size_t)e * DK, y + e);
+    for (int e = 0; e < DV / 2; ++e) z = fmaf(S[e], G[e], z);
 #pragma unroll
-      for (int e = 0; e < DV / 2; ++e) z = fmaf(X[e], y[e], z);
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-    }
-    if (mma_warp && lane == 0 && un < p.units) {
-      prefetch_l2_bulk(p.Sk + un * state_floats(DV), state_floats(DV) * 4);
-      prefetch_l2_bulk(p.Gk + un * state_floats(DV), state_floats(DV) * 4);
-    }
-    // the last unit's gradients have left their tiles
-    if (mma_warp && lane == 0) bulk_wait_read_all();
-    __syncthreads();
-    if (!mma_warp) {
-      if (lane == 0) F[F_Z + warp] = z;
-      term(OFF_E);
-      term(OFF_P);
-      term(OFF_T);
-      fence_proxy_async_smem();
-      if (warp < 4) {  // decays
-        const float a = i < len ? p.al.at(t0 + i, h) : 1.f;
-        const float pw = warp_prefix(a, lane);
-        F[F_A + i] = a;
-        F[F_SW + i] = warp_suffix(a, lane);
-        if (lane == 31) F[F_TOT + w4] = pw;
+    for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (lead) {
+      if (lane == 0 && un < p.units) {
+        prefetch_l2_bulk(p.Sk + un * state_floats(DV), state_floats(DV) * 4);
+        prefetch_l2_bulk(p.Gk + un * state_floats(DV), state_floats(DV) * 4);
       }
-    } else {
-      if ((ok = wait(B_LD, ph)) && elect_one()) {
+      ok = wait(B_LD, ph);
+      if (ok && elect_one()) {
         constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_S1, km(0, kk), km(1, kk), id, kk > 0);
@@ -596,6 +578,21 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       __syncwarp();
       issued = B_SC;
       issued_par = ph;
+      // the last unit's gradients have left their tiles
+      if (lane == 0) bulk_wait_read_all();
+    }
+    __syncthreads();
+    if (lane == 0) F[F_Z + warp] = z;
+    term(OFF_E, S);
+    term(OFF_P, S);
+    term(OFF_T, S);
+    fence_proxy_async_smem();
+    if (warp >= 4) {  // decays
+      const float a = i < len ? p.al.at(t0 + i, h) : 1.f;
+      const float pw = warp_prefix(a, lane);
+      F[F_A + i] = a;
+      F[F_SW + i] = warp_suffix(a, lane);
+      if (lane == 31) F[F_TOT + w4] = pw;
     }
     ok = __syncthreads_and(ok);
     if (!ok) break;
@@ -605,7 +602,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     const float pre = pw * (w4 > 0 ? tot.x : 1.f) * (w4 > 1 ? tot.y : 1.f) * (w4 > 2 ? tot.z : 1.f);
     const float suf = F[F_SW + i] * (w4 < 1 ? tot.y : 1.f) * (w4 < 2 ? tot.z : 1.f) *
                       (w4 < 3 ? tot.w : 1.f);
-    if (mma_warp) {
+    if (lead) {
       // dO S^T, the three terms of S one after another
       if (elect_one()) {
         constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
@@ -619,8 +616,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       __syncwarp();
       issued = B_DS;
       issued_par = ph;
-      ok = wait(B_DS, ph);
-    } else {
+    }
+    {
       // what lies past the sequence's end takes no part, finite or not (the
       // scores' products may read these rows before or after: rows and
       // columns that are masked)
@@ -639,12 +636,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
         fence_proxy_async_smem();
       }
-      // G's rows on their way while the products run
-      if (ok) {
-        states(p.Gk, u);
-        ok = wait(B_SC, ph) && wait(B_DS, ph);
-        tc_fence_after();
-      }
+      ok = ok && wait(B_SC, ph) && wait(B_DS, ph);
+      tc_fence_after();
     }
     ok = __syncthreads_and(ok);
     if (!ok) break;
@@ -652,8 +645,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     float intra = 0.f;
     // ---- E and P, the decays' sums within the chunk; x and dO S^T scaled; the
     // first term of G ----------------------------------------------------------------------
-    if (!mma_warp) {
-      term(OFF_T);
+    {
+      term(OFF_T, G);
       fence_proxy_async_smem();
       const bool in = i < len;
       // the decays between block J and this row's
@@ -787,7 +780,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
     // ---- K G and V G^T with G's first term; x; diag(pre) dO S^T ---------------------------
     constexpr uint32_t id_kg = idesc_bf16(128, DV, 0, 1), id_128 = idesc_bf16(128, 128, 0, 0);
-    if (mma_warp) {
+    if (lead) {
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -800,8 +793,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       __syncwarp();
       issued = B_G;
       issued_par = g3;
-      ok = wait(B_G, g3);
-    } else {
+    }
+    {
       if (hf == 0) {
 #pragma unroll
         for (int w = 1; w < 4; ++w)
@@ -810,7 +803,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       const float x = scale_rows<64>(row + TM_DQ + 64 * hf, pre, sm + OFF_Q, i, 64 * hf);
       F[F_X + 128 * hf + i] = i < len ? x : 0.f;
       ok = wait(B_G, g3);
-      term(OFF_T);
+      term(OFF_T, G);
       fence_proxy_async_smem();
       tc_fence_before();
     }
@@ -818,7 +811,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (!ok) break;
 
     // ---- second term; E K -----------------------------------------------------------------
-    if (mma_warp) {
+    if (lead) {
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -831,22 +824,25 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       __syncwarp();
       issued = B_G;
       issued_par = g3 + 1;
-      ok = wait(B_G, g3 + 1);
-    } else {
+    }
+    {
       if (hf == 0) {
         F[F_X + i] += F[F_X + 128 + i];
         F[F_IN + i] = intra;
       }
       ok = wait(B_G, g3 + 1);
-      term(OFF_T);
+      term(OFF_T, G);
       fence_proxy_async_smem();
-      if (un < p.units) states(p.Sk, un);  // in registers until the next unit
+      if (un < p.units) {  // in registers until the next unit
+        states(S, p.Sk, un);
+        states(G, p.Gk, un);
+      }
     }
     ok = __syncthreads_and(ok);
     if (!ok) break;
 
     // ---- third term; y; diag(suf) K G, diag(suf) V G^T --------------------------------------
-    if (mma_warp) {
+    if (lead) {
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
@@ -855,8 +851,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       __syncwarp();
       issued = B_G;
       issued_par = g3 + 2;
-      ok = wait(B_G, g3 + 2);
-    } else {
+    }
+    {
       ok = wait(B_G, g3 + 2);
       tc_fence_after();
       const float y = scale_rows<DV / 2>(row + TM_DV + DV / 2 * hf, suf, sm + OFF_V, i, DV / 2 * hf);
@@ -868,7 +864,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (!ok) break;
 
     // ---- P^T dO, E^T Q; the decays' gradient ------------------------------------------------
-    if (mma_warp) {
+    if (lead) {
       tc_fence_after();
       if (elect_one()) {
         constexpr uint32_t id_dv = idesc_bf16(128, DV, 1, 1), id_dk = idesc_bf16(128, 128, 1, 1);
@@ -881,15 +877,9 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       __syncwarp();
       issued = B_FIN;
       issued_par = ph;
-      ok = wait(B_FIN, ph);
-      loaded = false;
-      if (ok && un < p.units) {
-        if (lane == 0) load(t0n, hn);
-        loaded = true;
-        ld_par = ph ^ 1u;
-      }
-    } else {
-      if (warp == 0) {
+    }
+    {
+      if (warp == 4) {
         float a[4], c[4], b[4], v[4], y[4], hd[4], tl[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -933,6 +923,14 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       }
       ok = wait(B_FIN, ph);
       tc_fence_after();
+      if (lead) {
+        loaded = false;
+        if (ok && un < p.units) {
+          if (lane == 0) load(t0n, hn);
+          loaded = true;
+          ld_par = ph ^ 1u;
+        }
+      }
       // the gradients' rows: whole chunks leave by TMA from the tiles of E, P
       // and G's terms, a partial one row by row
       auto give = [&](uint32_t col, uint32_t off, __nv_bfloat16* g, int D, int n0, int nn) {
@@ -960,7 +958,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     }
     ok = __syncthreads_and(ok);
     if (!ok) break;
-    if (mma_warp && lane == 0 && len == C) {
+    if (lead && lane == 0 && len == C) {
       const int t = (int)t0;
       for (int x = 0; x < DK; x += 64) {
         tma_store_2d(&tm_dq, sb + OFF_E + 256 * x, h * DK + x, t);
@@ -977,11 +975,11 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     ph ^= 1u;
     g3 += 3;
   }
-  if (mma_warp && lane == 0) bulk_wait_all();
+  if (lead && lane == 0) bulk_wait_all();
   if (!ok) {
     set_status(p.status, CKDA_ERR_DEVICE_TIMEOUT);
     // loads and products in flight get their time
-    if (mma_warp) {
+    if (lead) {
       if (loaded) wait(B_LD, ld_par);
       if (issued != 0) wait(issued, issued_par);
     }
