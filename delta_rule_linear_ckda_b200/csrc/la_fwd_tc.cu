@@ -105,15 +105,16 @@ struct Args {
   float* Sf;
   int n_seqs, T, H, DV;
   int* status;
-  // segments per sequence; part[(n H + h) seg_n + g]: for g > 0 the end state
-  // of segment g - 1 (segment 0's from S0, the others' from zero), for g = 0
-  // a copy of S0; dec: the segments' decays
-  int seg_n;
+  // segments per sequence, and pieces per segment that the first launch takes
+  // (np = seg_n piece_n of them); part[(n H + h) np + g]: for g > 0 the end
+  // state of piece g - 1 (piece 0's from S0, the others' from zero), for
+  // g = 0 a copy of S0; dec: the pieces' decays
+  int seg_n, piece_n;
   float* part;
   float* dec;
 };
 
-// SUM: the segments' own end states only (segments 0 .. seg_n - 2)
+// SUM: the pieces' own end states only (those of segments 0 .. seg_n - 2)
 template <typename Tout, bool SUM>
 __global__ void __launch_bounds__(kThreads, 1)
 la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
@@ -131,7 +132,8 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   }
 
   const int slices = p.DV / BV;
-  const int nseg = SUM ? p.seg_n - 1 : p.seg_n;
+  const int np = p.seg_n * p.piece_n;
+  const int nseg = SUM ? np - p.piece_n : p.seg_n;
   // block index: column slice, then segment, then head, then sequence (longest first)
   int b = blockIdx.x;
   const int j0 = (b % slices) * BV;
@@ -176,9 +178,10 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __shfl_sync(0xffffffffu, *reinterpret_cast<volatile uint32_t*>(sm + OFF_MISC), 0);
 
   const int nck_all = (int)((sr.end - sr.begin + C - 1) / C);
-  const int cbeg = (int)((int64_t)seg * nck_all / p.seg_n);
+  const int parts = SUM ? np : p.seg_n;  // (a segment ends where its last piece does)
+  const int cbeg = (int)((int64_t)seg * nck_all / parts);
   const int nck =
-      __shfl_sync(0xffffffffu, (int)((int64_t)(seg + 1) * nck_all / p.seg_n) - cbeg, 0);
+      __shfl_sync(0xffffffffu, (int)((int64_t)(seg + 1) * nck_all / parts) - cbeg, 0);
   const int64_t tok0 = sr.begin + (int64_t)cbeg * C;
   auto len_of = [&](int c) -> int {
     const int64_t left = sr.end - (tok0 + (int64_t)c * C);
@@ -326,15 +329,15 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const size_t unit = (size_t)n * p.H + h;
     const size_t at = ((size_t)r * p.DV) + j0 + kHalf * hf;  // this thread's columns of a state
     const size_t stsz = (size_t)DK * p.DV;
-    float* part = p.part + unit * p.seg_n * stsz + at;
+    float* part = p.part + unit * np * stsz + at;
     {
       // segment 0 starts from S0; with segments, from a copy of it that the
       // first launch keeps (the last segment may write S_final over S0 before
-      // this block starts); segment g from the decayed sum of the end states
-      // before it
+      // this block starts); the others from the decayed sum of the pieces' end
+      // states before them
       float f = 1.f;
 #pragma unroll 1
-      for (int g = seg; g >= 0; --g) {
+      for (int g = SUM ? seg : seg * p.piece_n; g >= 0; --g) {
         const float* src = nullptr;
         if (g > 0)
           src = SUM ? nullptr : part + g * stsz;
@@ -350,7 +353,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             S[e + 3] = fmaf(f, x.w, S[e + 3]);
           }
         }
-        if (!SUM && g > 0) f *= p.dec[unit * p.seg_n + g - 1];
+        if (!SUM && g > 0) f *= p.dec[unit * np + g - 1];
       }
       if (SUM && seg == 0 && p.S0 != nullptr) store_cols<kHalf>(part, S);
     }
@@ -448,7 +451,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     if (ok) {
       if (SUM) {
         store_cols<kHalf>(part + (seg + 1) * stsz, S);
-        if (r == 0 && hf == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = total;
+        if (r == 0 && hf == 0 && j0 == 0) p.dec[unit * np + seg] = total;
       } else if (p.Sf != nullptr && seg == p.seg_n - 1) {
         store_cols<kHalf>(p.Sf + unit * stsz + at, S);
       }
@@ -657,6 +660,12 @@ static int fwd_segments(int n_seqs, int T, int H, int dv, bool varlen) {
   return g < 1 ? 1 : (int)g;
 }
 
+// The first launch leaves the last segment out: smaller pieces fill the SMs.
+static int fwd_pieces(int n_seqs, int H, int dv, int segs) {
+  const int64_t ctas = (int64_t)n_seqs * H * (dv / fw::BV) * (segs - 1);
+  return segs == 1 ? 1 : (int)(148 / ctas > 8 ? 8 : 148 / ctas < 1 ? 1 : 148 / ctas);
+}
+
 }  // namespace la
 
 bool la_fwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen) {
@@ -668,7 +677,8 @@ bool la_fwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bo
 
 size_t la_fwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen) {
   const int g = la::fwd_segments(n_seqs, T, H, dv, varlen);
-  return g > 1 ? (size_t)n_seqs * H * g * ((size_t)dk * dv + 64) * 4 : 0;
+  const int np = g * la::fwd_pieces(n_seqs, H, dv, g);
+  return g > 1 ? (size_t)n_seqs * H * np * ((size_t)dk * dv + 64) * 4 : 0;
 }
 
 cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const void* k,
@@ -687,16 +697,17 @@ cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const
   if (out_dtype == CKDA_BF16 && !bf16_map(&mo, out, (uint64_t)H * dv, rows, fw::C))
     return cudaErrorInvalidValue;
   const int g = fwd_segments(n_seqs, T, H, dv, varlen);
-  fw::Args a{{alpha, H, per_head}, S0, cu, out, S_final, n_seqs, T, H, dv, status, g, nullptr,
-             nullptr};
+  const int np = g * fwd_pieces(n_seqs, H, dv, g);
+  fw::Args a{{alpha, H, per_head}, S0, cu, out, S_final, n_seqs, T, H, dv, status, g, np / g,
+             nullptr, nullptr};
   const unsigned units = (unsigned)n_seqs * H * (dv / fw::BV);
   cudaError_t e;
   if (g > 1) {
     a.part = static_cast<float*>(ws);
-    a.dec = a.part + (size_t)n_seqs * H * g * dk * dv;
+    a.dec = a.part + (size_t)n_seqs * H * np * dk * dv;
     auto ks = fw::la_fwd_kernel<float, true>;
     if ((e = max_smem<0>(ks, fw::kSmem)) != cudaSuccess) return e;
-    ks<<<units * (g - 1), fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
+    ks<<<units * (np - np / g), fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   if (out_dtype == CKDA_BF16) {
