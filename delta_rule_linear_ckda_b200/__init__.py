@@ -22,7 +22,8 @@ def __getattr__(name):
         from . import api
 
         api._lib.load()
-        return getattr(api, name)
+        fn = globals()[name] = getattr(api, name)  # found directly from now on
+        return fn
     if name == "CKDAError":
         from ._lib import CKDAError
 

@@ -546,10 +546,22 @@ def sfda_decode_step(q, k, v, alpha, theta, beta, S, out=None, out_dtype=None) -
 
 # ---- head-decay linear attention ------------------------------------------------
 
-# A call's checks and its launch take about 10 us on the host, as long as the
-# smallest kernels: the usual case is one expression per tensor (``_need`` words
-# the error), and the current device is set only when it is another one.
+# A call's checks and its launch cost the host as much time as the smallest
+# kernels take: the usual case is one pass over the tensors (``_check``, where
+# that finds something, words the error), and the current device is set only
+# when it is another one.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_CF = torch.contiguous_format
+
+
+def _plain(ix, dtype, *tensors):
+    """Whether all are contiguous tensors of ``dtype`` on CUDA device ``ix``."""
+    for t in tensors:
+        if type(t) is not torch.Tensor or t.dtype is not dtype or t.get_device() != ix \
+                or not t.is_contiguous():
+            return False
+    return ix >= 0
 
 
 def _check(t, name, dtype, dev):
@@ -558,16 +570,13 @@ def _check(t, name, dtype, dev):
         _need(t, name, dtype, dev)
 
 
-def _stream_of(dev):
-    return _raw_stream(dev.index) if _raw_stream is not None else _stream_ptr(dev)
-
-
 def _call(fn, dev, *args):
     """``fn(*args, stream)`` with ``dev`` as the current device."""
-    if torch.cuda.current_device() == dev.index:
-        return fn(*args, _stream_of(dev))
-    with torch.cuda.device(dev):
-        return fn(*args, _stream_of(dev))
+    ix = dev.index
+    if ix != _current():
+        with torch.cuda.device(dev):
+            return fn(*args, _stream_ptr(dev))
+    return fn(*args, _raw_stream(ix) if _raw_stream is not None else _stream_ptr(dev))
 
 
 def _la_inputs(q, k, v, alpha, cu_seqlens):
@@ -575,9 +584,11 @@ def _la_inputs(q, k, v, alpha, cu_seqlens):
     dev = q.device
     if q.dtype not in _DT:
         raise TypeError("q, k, v must be float32 or bfloat16")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check(t, name, q.dtype, dev)
-    _check(alpha, "alpha", torch.float32, dev)
+    ix = q.get_device()
+    if not (_plain(ix, q.dtype, q, k, v) and _plain(ix, torch.float32, alpha)):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _check(t, name, q.dtype, dev)
+        _check(alpha, "alpha", torch.float32, dev)
     if cu_seqlens is None:
         if q.dim() != 4:
             raise ValueError("q must be [B, T, H, dk]")
@@ -633,7 +644,7 @@ def la_fwd_chunked(q, k, v, alpha, S0=None, cu_seqlens=None, out=None, S_final=N
     if out_dtype not in _DT:
         raise TypeError("out_dtype must be float32 or bfloat16")
     if out is None:
-        out = torch.empty(v.shape, dtype=out_dtype, device=dev)
+        out = torch.empty_like(v, dtype=out_dtype, memory_format=_CF)
     else:
         _check(out, "out", out_dtype, dev)
         if out.shape != v.shape:
@@ -649,8 +660,8 @@ def la_fwd_chunked(q, k, v, alpha, S0=None, cu_seqlens=None, out=None, S_final=N
         _check(workspace, "workspace", torch.uint8, dev)
     rc = _call(
         _lib.load().ckda_la_fwd_chunked, dev,
-        _p(q), _p(k), _p(v), _p(alpha), _p(S0), _p(cu_seqlens), _p(out), _p(S_final), B, T, H,
-        dk, dv, 1 if per_head else 0, _DT[q.dtype], _DT[out_dtype], _p(workspace),
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), _p(S0), _p(cu_seqlens),
+        out.data_ptr(), _p(S_final), B, T, H, dk, dv, 1 if per_head else 0, _DT[q.dtype], _DT[out_dtype], _p(workspace),
         0 if workspace is None else workspace.numel())
     if rc != 0:
         raise CKDAError(rc, "ckda_la_fwd_chunked")
@@ -723,10 +734,12 @@ def la_decode_step(q, k, v, alpha, S, out=None, out_dtype=None) -> torch.Tensor:
     dev, dtype = q.device, q.dtype
     if dtype not in _DT:
         raise TypeError("q, k, v must be float32 or bfloat16")
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _check(t, name, dtype, dev)
-    _check(S, "S", torch.float32, dev)
-    _check(alpha, "alpha", torch.float32, dev)
+    ix = q.get_device()
+    if not (_plain(ix, dtype, q, k, v) and _plain(ix, torch.float32, S, alpha)):
+        for name, t in (("q", q), ("k", k), ("v", v)):
+            _check(t, name, dtype, dev)
+        _check(S, "S", torch.float32, dev)
+        _check(alpha, "alpha", torch.float32, dev)
     if S.dim() != 4 or q.shape != S.shape[:3] or k.shape != q.shape or \
             v.shape != S.shape[:2] + S.shape[3:]:
         raise ValueError("q, k must be [B, H, dk], v [B, H, dv] and S [B, H, dk, dv]")
@@ -739,15 +752,15 @@ def la_decode_step(q, k, v, alpha, S, out=None, out_dtype=None) -> torch.Tensor:
     if out_dtype not in _DT:
         raise TypeError("out_dtype must be float32 or bfloat16")
     if out is None:
-        out = torch.empty_like(v, dtype=out_dtype)
+        out = torch.empty_like(v, dtype=out_dtype, memory_format=_CF)
     else:
         _check(out, "out", out_dtype, dev)
         if out.shape != v.shape:
             raise ValueError("out must have v's shape")
     rc = _call(
         _lib.load().ckda_la_decode_step, dev,
-        _p(q), _p(k), _p(v), _p(alpha), _p(S), _p(out), B, H, dk, dv, 1 if per_head else 0,
-        _DT[q.dtype], _DT[out_dtype])
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), alpha.data_ptr(), S.data_ptr(), out.data_ptr(),
+        B, H, dk, dv, 1 if per_head else 0, _DT[dtype], _DT[out_dtype])
     if rc != 0:
         raise CKDAError(rc, "ckda_la_decode_step")
     return out
@@ -762,8 +775,10 @@ def _token_stride(t, name):
     """Elements between the tokens of ``[..., H, d]``: the heads of a token lie together, the
     tokens at one distance (a view into a wider projection)."""
     H, d = t.shape[-2:]
-    if t.numel() == 0:
+    if t.is_contiguous() or t.numel() == 0:
         return H * d
+    if t.dim() == 3 and t.stride(2) == 1 and (t.stride(1) == d or H == 1):
+        return t.stride(0) if t.shape[0] > 1 else H * d
     if t.stride(-1) != 1 or (H > 1 and t.stride(-2) != d):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     step, span = None, None
@@ -786,31 +801,33 @@ def _qk_inputs(q, k, wq, wk, positions, inv_freq, norm):
             raise TypeError(f"{name} must be a torch.Tensor")
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
-    dev = q.device
+    dev, ix = q.device, q.get_device()
     if q.dtype not in _DT:
         raise TypeError("q, k must be float32 or bfloat16")
-    if k.dtype != q.dtype or k.device != dev:
+    if k.dtype != q.dtype or k.get_device() != ix:
         raise ValueError("q and k must share a dtype and a device")
-    if q.dim() < 3 or k.dim() != q.dim() or k.shape[:-2] != q.shape[:-2] or \
-            k.shape[-1] != q.shape[-1]:
+    qs, ks = q.shape, k.shape
+    if len(qs) < 3 or len(ks) != len(qs) or ks[:-2] != qs[:-2] or ks[-1] != qs[-1]:
         raise ValueError("q and k must be [..., H, d] with the same tokens and d")
     if norm not in _NORM:
         raise ValueError("norm must be 'l2' or 'rms'")
-    lead, (Hq, d), Hk = q.shape[:-2], q.shape[-2:], k.shape[-2]
+    lead, (Hq, d), Hk = qs[:-2], qs[-2:], ks[-2]
     for name, w in (("wq", wq), ("wk", wk)):
         if w is not None:
-            _check(w, name, torch.float32, dev)
+            if not _plain(ix, torch.float32, w):
+                _check(w, name, torch.float32, dev)
             if w.shape != (d,):
                 raise ValueError(f"{name} must be [{d}]")
     rot = 0
     if (positions is None) != (inv_freq is None):
         raise ValueError("positions and inv_freq come together")
     if positions is not None:
-        _check(positions, "positions", torch.int32, dev)
-        _check(inv_freq, "inv_freq", torch.float32, dev)
+        if not (_plain(ix, torch.int32, positions) and _plain(ix, torch.float32, inv_freq)):
+            _check(positions, "positions", torch.int32, dev)
+            _check(inv_freq, "inv_freq", torch.float32, dev)
         if positions.shape != lead or inv_freq.dim() != 1:
             raise ValueError("positions must have the tokens' shape and inv_freq be [rot / 2]")
-        rot = 2 * inv_freq.numel()
+        rot = 2 * inv_freq.shape[0]
     return math.prod(lead), Hq, Hk, d, rot, _token_stride(q, "q"), _token_stride(k, "k")
 
 
@@ -836,7 +853,7 @@ def qk_norm_rope(q, k, wq=None, wk=None, positions=None, inv_freq=None, norm: st
     outs = []
     for name, t, x in (("q_out", q_out, q), ("k_out", k_out, k)):
         if t is None:
-            t = torch.empty(x.shape, dtype=out_dtype, device=dev)
+            t = torch.empty_like(x, dtype=out_dtype, memory_format=_CF)
         else:
             _check(t, name, out_dtype, dev)
             if t.shape != x.shape:
@@ -844,8 +861,8 @@ def qk_norm_rope(q, k, wq=None, wk=None, positions=None, inv_freq=None, norm: st
         outs.append(t)
     rc = _call(
         _lib.load().ckda_qk_norm_rope, dev,
-        _p(q), _p(k), _p(wq), _p(wk), _p(positions), _p(inv_freq), _p(outs[0]), _p(outs[1]),
-        n, Hq, Hk, d, rot, 1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype],
+        q.data_ptr(), k.data_ptr(), _p(wq), _p(wk), _p(positions), _p(inv_freq),
+        outs[0].data_ptr(), outs[1].data_ptr(), n, Hq, Hk, d, rot, 1 if interleaved else 0, _NORM[norm], eps, qs, ks, _DT[q.dtype],
         _DT[out_dtype])
     if rc != 0:
         raise CKDAError(rc, "ckda_qk_norm_rope")
@@ -862,14 +879,15 @@ def qk_norm_rope_bwd(q, k, dq_out, dk_out, wq=None, wk=None, positions=None, inv
     ``[d]``, each None without its weight)."""
     n, Hq, Hk, d, rot, qs, ks = _qk_inputs(q, k, wq, wk, positions, inv_freq, norm)
     dev = q.device
+    plain = _plain(q.get_device(), q.dtype, dq_out, dk_out)
     for name, t, x in (("dq_out", dq_out, q), ("dk_out", dk_out, k)):
-        _check(t, name, q.dtype, dev)
+        if not plain:
+            _check(t, name, q.dtype, dev)
         if t.shape != x.shape:
             raise ValueError(f"{name} must have {name[1]}'s shape")
-    g = {"dq": torch.empty(q.shape, dtype=q.dtype, device=dev),
-         "dk": torch.empty(k.shape, dtype=q.dtype, device=dev),
-         "dwq": None if wq is None else torch.empty(d, dtype=torch.float32, device=dev),
-         "dwk": None if wk is None else torch.empty(d, dtype=torch.float32, device=dev)}
+    g = {"dq": torch.empty_like(q, memory_format=_CF), "dk": torch.empty_like(k, memory_format=_CF),
+         "dwq": None if wq is None else torch.empty_like(wq),
+         "dwk": None if wk is None else torch.empty_like(wk)}
     lib = _lib.load()
     if workspace is None and (wq is not None or wk is not None):
         need = lib.ckda_qk_norm_rope_bwd_workspace_bytes(d)
