@@ -52,8 +52,8 @@ constexpr int kHalf = BV / 2;
 constexpr uint32_t OFF_A = 0;                     // k or q [128][128]
 constexpr uint32_t OFF_B = 32768;                 // v or do [128][64]
 constexpr uint32_t OFF_VW = OFF_B + 16384;        // diag(w) of it, three terms
-constexpr uint32_t OFF_DEC = OFF_VW + 3 * 16384;  // 2 x {a[128], sufW[128], tot[4]}
-constexpr uint32_t kDecBytes = 1024 + 16;
+constexpr uint32_t OFF_DEC = OFF_VW + 3 * 16384;  // 2 x the decays (put_decays)
+constexpr uint32_t kDecBytes = kDecFloats * 4;
 constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
 constexpr uint32_t B_A = 0, B_B = 8, B_VW = 16, B_D = 24, B_DEC = 32, B_DECE = 48;
 constexpr uint32_t OFF_MISC = OFF_BAR + 64;
@@ -201,7 +201,7 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       else
         wgt = dc[128 + r] * (q4 < 1 ? tot.y : 1.f) * (q4 < 2 ? tot.z : 1.f) *
               (q4 < 3 ? tot.w : 1.f);
-      gamma = (tot.x * tot.y) * (tot.z * tot.w);
+      gamma = dc[260];
       arrive(B_DECE + 8 * (it & 1));
       if (!(ok = wait(B_B, it))) break;
       if (len < C && !(ok = wait(B_A, it))) break;
@@ -307,15 +307,9 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     for (int it = 0; it < nck; ++it) {
       load(it + 1, nx);
       if (it >= 2 && !(ok = wait(B_DECE + 8 * (it & 1), (it >> 1) - 1))) break;
-      float* o = reinterpret_cast<float*>(sm + OFF_DEC) + (it & 1) * (kDecBytes / 4);
+      put_decays(reinterpret_cast<float*>(sm + OFF_DEC) + (it & 1) * kDecFloats, a, lane);
 #pragma unroll
-      for (int bk = 0; bk < 4; ++bk) {
-        const float pw = warp_prefix(a[bk], lane), sw = warp_suffix(a[bk], lane);
-        o[32 * bk + lane] = a[bk];
-        o[128 + 32 * bk + lane] = sw;
-        if (lane == 31) o[256 + bk] = pw;
-        a[bk] = nx[bk];
-      }
+      for (int bk = 0; bk < 4; ++bk) a[bk] = nx[bk];
       arrive(B_DEC + 8 * (it & 1));
     }
   }

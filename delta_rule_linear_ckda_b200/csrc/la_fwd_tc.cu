@@ -61,8 +61,8 @@ constexpr uint32_t OFF_K = 65536;                // 2 stages, the same
 constexpr uint32_t OFF_V = 131072;               // 2 stages [128][64]
 constexpr uint32_t OFF_VW = 163840;              // diag(suf) V: 3 terms [128][64]
 constexpr uint32_t OFF_SB = OFF_VW + 3 * 16384;  // bf16 state [128][64]
-constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x {a[128], sufW[128], tot[4]} fp32
-constexpr uint32_t kDecBytes = 1024 + 16;
+constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x the decays (put_decays)
+constexpr uint32_t kDecBytes = kDecFloats * 4;
 constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
 constexpr uint32_t OFF_MISC = OFF_BAR + 176;     // tensor-memory base, the sequence
 constexpr uint32_t kSmem = OFF_MISC + 16;
@@ -392,7 +392,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         const float4 tot = *reinterpret_cast<const float4*>(tots(c));
         const float wgt = suff(c)[r] * (q4 < 1 ? tot.y : 1.f) * (q4 < 2 ? tot.z : 1.f) *
                           (q4 < 3 ? tot.w : 1.f);
-        gamma = (tot.x * tot.y) * (tot.z * tot.w);
+        gamma = decs(c)[260];
         arrive(B_DECE + 8 * st);
         if (!(ok = wait(B_V + 8 * st, c >> 1))) break;
         if (len < C && !(ok = wait(B_K + 8 * st, c >> 1))) break;
@@ -627,15 +627,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     for (int c = 0; c < nck; ++c) {
       load(c + 1, nx);
       if (c >= 2 && !(ok = wait(B_DECE + 8 * (c & 1), (c >> 1) - 1))) break;
-      float* o = reinterpret_cast<float*>(sm + OFF_DEC) + (c & 1) * (kDecBytes / 4);
+      put_decays(reinterpret_cast<float*>(sm + OFF_DEC) + (c & 1) * kDecFloats, a, lane);
 #pragma unroll
-      for (int bk = 0; bk < 4; ++bk) {
-        const float pw = warp_prefix(a[bk], lane), sw = warp_suffix(a[bk], lane);
-        o[32 * bk + lane] = a[bk];
-        o[128 + 32 * bk + lane] = sw;
-        if (lane == 31) o[256 + bk] = pw;
-        a[bk] = nx[bk];
-      }
+      for (int bk = 0; bk < 4; ++bk) a[bk] = nx[bk];
       arrive(B_DEC + 8 * (c & 1));
     }
   }

@@ -32,24 +32,46 @@ __device__ __forceinline__ int longest_first(const int32_t* cu, int n_seqs, int 
 }
 
 // Products over a warp's lanes: through this lane, and behind it.
-__device__ __forceinline__ float warp_prefix(float a, int lane) {
+template <typename T>
+__device__ __forceinline__ T warp_prefix(T a, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float b = __shfl_up_sync(0xffffffffu, a, o);
+    const T b = __shfl_up_sync(0xffffffffu, a, o);
     a = lane >= o ? a * b : a;
   }
   return a;
 }
 
-__device__ __forceinline__ float warp_suffix(float a, int lane) {
-  float s = __shfl_down_sync(0xffffffffu, a, 1);
-  s = lane == 31 ? 1.f : s;
+template <typename T>
+__device__ __forceinline__ T warp_suffix(T a, int lane) {
+  T s = __shfl_down_sync(0xffffffffu, a, 1);
+  s = lane == 31 ? T(1) : s;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const float b = __shfl_down_sync(0xffffffffu, s, o);
+    const T b = __shfl_down_sync(0xffffffffu, s, o);
     s = lane + o < 32 ? s * b : s;
   }
   return s;
+}
+
+// A chunk's decays (four blocks of 32 tokens, a lane one of each) for the other
+// warps: {a[128], sufW[128], tot[4], gamma}.  The products are taken in 64 bits
+// and rounded once: in 32 bits their errors all lie on one side when the decay
+// is the same for every token, and add up over a long state (1e-6 of S_final
+// after 4096 tokens instead of 2e-7).
+constexpr int kDecFloats = 264;
+__device__ __forceinline__ void put_decays(float* o, const float* a, int lane) {
+  double all = 1.0;
+#pragma unroll
+  for (int bk = 0; bk < 4; ++bk) {
+    const double x = (double)a[bk];
+    const double pw = warp_prefix(x, lane), sw = warp_suffix(x, lane);
+    o[32 * bk + lane] = a[bk];
+    o[128 + 32 * bk + lane] = (float)sw;
+    if (lane == 31) o[256 + bk] = (float)pw;
+    all *= pw;
+  }
+  if (lane == 31) o[260] = (float)all;
 }
 
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }
