@@ -1,5 +1,5 @@
 // Backward of head-decay linear attention on the tensor cores (tcgen05): bf16
-// inputs, d_k = 128, d_v 64 or 128 (sm_100a).
+// inputs, d_k and d_v 64 or 128 (sm_100a).
 //
 // Per chunk of C = 128 tokens, S the state at its start, G the adjoint of the
 // state at its end, D(i, j) = a_{j+1} .. a_i (zero for j > i):
@@ -39,7 +39,7 @@ constexpr int C = 128;
 constexpr int DK = 128;
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 
-// A state in the workspace: columns in groups of four, [d_v / 4][128 rows][4],
+// A state in the workspace (always 128 rows): columns in groups of four, [d_v / 4][128 rows][4],
 // so that a warp whose lanes are rows reads and writes whole lines.
 __host__ __device__ constexpr size_t state_floats(int dv) { return (size_t)DK * dv; }
 
@@ -71,6 +71,8 @@ struct Args {
   int* status;
 };
 
+// KD: d_k
+template <int KD>
 __global__ void __launch_bounds__(kThreads, 2)
 la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                  const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -113,6 +115,11 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     tmem_alloc(sb + OFF_MISC, kTmemCols);
     tmem_relinquish();
   }
+  if constexpr (KD < DK) {  // no load writes a's second 64 columns
+    for (int e = tid; e < 1024; e += kThreads)
+      *reinterpret_cast<uint4*>(sm + OFF_A + 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -144,7 +151,8 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
     const int q4 = warp & 3, hf = warp >> 2;
     const int r = 32 * q4 + lane;
     const uint32_t row = tmem + ((uint32_t)(32 * q4) << 16);
-    const size_t unit = (size_t)n * p.H + h, stsz = state_floats(p.DV);
+    const size_t unit = (size_t)n * p.H + h, stsz = (size_t)KD * p.DV;
+    const bool row_in = KD == DK || r < KD;
     const size_t at = (size_t)r * p.DV + j0 + kHalf * hf;
     float S[kHalf];
     {
@@ -152,7 +160,8 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
 #pragma unroll
       for (int e = 0; e < kHalf; e += 4) {
         float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (src != nullptr) x = *reinterpret_cast<const float4*>(src + unit * stsz + at + e);
+        if (src != nullptr && row_in)
+          x = *reinterpret_cast<const float4*>(src + unit * stsz + at + e);
         S[e] = x.x; S[e + 1] = x.y; S[e + 2] = x.z; S[e + 3] = x.w;
       }
     }
@@ -184,7 +193,7 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
       }
       if (it == nck) break;
       {
-        float* o = kept + ((size_t)(slot0 + chunk(it)) * p.H + h) * stsz;
+        float* o = kept + ((size_t)(slot0 + chunk(it)) * p.H + h) * state_floats(p.DV);
 #pragma unroll
         for (int e = 0; e < kHalf; e += 4)
           *reinterpret_cast<float4*>(o + (size_t)e * DK) =
@@ -234,14 +243,14 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
             *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 +
                                       sw128_chunk(r, kHalf * hf + 8 * c8, 128)) = z;
 #pragma unroll 1
-        for (int c8 = 0; c8 < DK / 16; ++c8)
-          *reinterpret_cast<uint4*>(sm + OFF_A + sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
+        for (int c8 = 0; c8 < KD / 16; ++c8)
+          *reinterpret_cast<uint4*>(sm + OFF_A + sw128_chunk(r, (KD / 2) * hf + 8 * c8, 128)) = z;
       }
       fence_proxy_async_smem();
       tc_fence_before();
       arrive(B_VW);
     }
-    if (ok && rev && p.dS0 != nullptr) store_cols<kHalf>(p.dS0 + unit * stsz + at, S);
+    if (ok && rev && p.dS0 != nullptr && row_in) store_cols<kHalf>(p.dS0 + unit * stsz + at, S);
   } else if (warp == 8) {
     // ---- MMA (the whole warp waits, one lane issues) ---------------------------------------
     const uint64_t d_a = smem_desc(sb + OFF_A, 16384, 1024, kSwizzle128);
@@ -275,14 +284,13 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
         par_last = it;
         if (it + 1 < nck) {
           const int t1 = (int)tok(it + 1);
-          tma_prefetch_2d(tm_a, h * DK, t1);
-          tma_prefetch_2d(tm_a, h * DK + 64, t1);
+          for (int x = 0; x < KD; x += 64) tma_prefetch_2d(tm_a, h * KD + x, t1);
           tma_prefetch_2d(tm_b, h * p.DV + j0, t1);
         }
         if (it > 0 && !(ok = wait(B_D, it - 1))) break;
-        mbar_expect_tx(bar + B_A, 32768);
-        tma_load_2d(sb + OFF_A, tm_a, h * DK, t, bar + B_A);
-        tma_load_2d(sb + OFF_A + 16384, tm_a, h * DK + 64, t, bar + B_A);
+        mbar_expect_tx(bar + B_A, 256 * KD);
+        for (int x = 0; x < KD; x += 64)
+          tma_load_2d(sb + OFF_A + 256 * x, tm_a, h * KD + x, t, bar + B_A);
         open_a = true;
       }
       if (!ok) {  // give the loads in flight their time
@@ -433,7 +441,7 @@ __device__ __forceinline__ float scale_rows(uint32_t addr, float f, const uint8_
   return s;
 }
 
-template <int DV>
+template <int KD, int DV>  // d_k, d_v
 __global__ void __launch_bounds__(kThreads, 1)
 la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -481,10 +489,10 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   };
   auto load = [&](int64_t t0, int h) {
     const int t = (int)t0;
-    mbar_expect_tx(bar + B_LD, 65536 + 2 * 128 * DV * 2);
-    for (int x = 0; x < DK; x += 64) {
-      tma_load_2d(sb + OFF_Q + 256 * x, &tm_q, h * DK + x, t, bar + B_LD);
-      tma_load_2d(sb + OFF_K + 256 * x, &tm_k, h * DK + x, t, bar + B_LD);
+    mbar_expect_tx(bar + B_LD, 2 * 256 * (KD + DV));
+    for (int x = 0; x < KD; x += 64) {
+      tma_load_2d(sb + OFF_Q + 256 * x, &tm_q, h * KD + x, t, bar + B_LD);
+      tma_load_2d(sb + OFF_K + 256 * x, &tm_k, h * KD + x, t, bar + B_LD);
     }
     for (int x = 0; x < DV; x += 64) {
       tma_load_2d(sb + OFF_DO + 256 * x, &tm_do, h * DV + x, t, bar + B_LD);
@@ -518,7 +526,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
   float S[DV / 2], G[DV / 2];
   const size_t mine = (size_t)(DV / 2 * hf) * DK + 4 * i;
   auto states = [&](float (&X)[DV / 2], const float* kept, int64_t w) {
-    const float* a = kept + w * state_floats(DV) + mine;
+    const float* a = kept + w * state_floats(DV) + mine;  // (rows behind d_k are zero there)
 #pragma unroll
     for (int e = 0; e < DV / 2; e += 4) ld4(a + (size_t)e * DK, X + e);
   };
@@ -564,7 +572,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       if (ok && elect_one()) {
         constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_S1, km(0, kk), km(1, kk), id, kk > 0);
+        for (int kk = 0; kk < KD / 16; ++kk)
+          mma_f16(tmem + TM_S1, km(0, kk), km(1, kk), id, kk > 0);
 #pragma unroll
         for (int kk = 0; kk < DV / 16; ++kk) mma_f16(tmem + TM_S2, km(3, kk), km(2, kk), id, kk > 0);
         mma_commit(bar + B_SC);
@@ -599,7 +608,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (lead) {
       // dO S^T, the three terms of S one after another
       if (elect_one()) {
-        constexpr uint32_t id = idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t id = idesc_bf16(128, KD, 0, 0);
 #pragma unroll 1
         for (int e = 0; e < 3; ++e)
 #pragma unroll
@@ -619,9 +628,9 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       if (ok && i >= len) {
         const uint4 zz = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll 1
-        for (int e = 0; e < DK / 16; ++e) {
-          *reinterpret_cast<uint4*>(sm + OFF_Q + sw128_chunk(i, DK / 2 * hf + 8 * e, 128)) = zz;
-          *reinterpret_cast<uint4*>(sm + OFF_K + sw128_chunk(i, DK / 2 * hf + 8 * e, 128)) = zz;
+        for (int e = 0; e < KD / 16; ++e) {
+          *reinterpret_cast<uint4*>(sm + OFF_Q + sw128_chunk(i, KD / 2 * hf + 8 * e, 128)) = zz;
+          *reinterpret_cast<uint4*>(sm + OFF_K + sw128_chunk(i, KD / 2 * hf + 8 * e, 128)) = zz;
         }
 #pragma unroll 1
         for (int e = 0; e < DV / 16; ++e) {
@@ -773,15 +782,16 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (!ok) break;
 
     // ---- K G and V G^T with G's first term; x; diag(pre) dO S^T ---------------------------
-    constexpr uint32_t id_kg = idesc_bf16(128, DV, 0, 1), id_128 = idesc_bf16(128, 128, 0, 0);
+    constexpr uint32_t id_kg = idesc_bf16(128, DV, 0, 1), id_vg = idesc_bf16(128, KD, 0, 0);
     if (lead) {
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, kk > 0);
+        for (int kk = 0; kk < KD / 16; ++kk)
+          mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, kk > 0);
 #pragma unroll
         for (int kk = 0; kk < DV / 16; ++kk)
-          mma_f16(tmem + TM_DK, km(2, kk), km(6, kk), id_128, kk > 0);
+          mma_f16(tmem + TM_DK, km(2, kk), km(6, kk), id_vg, kk > 0);
         mma_commit(bar + B_G);
       }
       __syncwarp();
@@ -794,7 +804,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         for (int w = 1; w < 4; ++w)
           if (w > w4) intra += F[F_COL + 32 * (w * (w - 1) / 2 + w4) + lane];
       }
-      const float x = scale_rows<64>(row + TM_DQ + 64 * hf, pre, sm + OFF_Q, i, 64 * hf);
+      const float x = scale_rows<KD / 2>(row + TM_DQ + KD / 2 * hf, pre, sm + OFF_Q, i, KD / 2 * hf);
       F[F_X + 128 * hf + i] = i < len ? x : 0.f;
       ok = wait(B_G, g3);
       term(OFF_T, G);
@@ -809,9 +819,10 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
+        for (int kk = 0; kk < KD / 16; ++kk)
+          mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
         mma_commit(bar + B_G);
-        constexpr uint32_t id = idesc_bf16(128, 128, 0, 1);
+        constexpr uint32_t id = idesc_bf16(128, KD, 0, 1);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DQ, km(4, kk), mn(1, kk), id, 1u);
       }
@@ -839,7 +850,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (lead) {
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
+        for (int kk = 0; kk < KD / 16; ++kk)
+          mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
         mma_commit(bar + B_G);
       }
       __syncwarp();
@@ -851,7 +863,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       tc_fence_after();
       const float y = scale_rows<DV / 2>(row + TM_DV + DV / 2 * hf, suf, sm + OFF_V, i, DV / 2 * hf);
       F[(hf ? F_Y1 : F_Y0) + i] = i < len ? y : 0.f;
-      scale_rows<64>(row + TM_DK + 64 * hf, suf, nullptr, i, 0);
+      scale_rows<KD / 2>(row + TM_DK + KD / 2 * hf, suf, nullptr, i, 0);
       tc_fence_before();
     }
     ok = __syncthreads_and(ok);
@@ -861,7 +873,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (lead) {
       tc_fence_after();
       if (elect_one()) {
-        constexpr uint32_t id_dv = idesc_bf16(128, DV, 1, 1), id_dk = idesc_bf16(128, 128, 1, 1);
+        constexpr uint32_t id_dv = idesc_bf16(128, DV, 1, 1), id_dk = idesc_bf16(128, KD, 1, 1);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, mn(5, kk), mn(3, kk), id_dv, 1u);
 #pragma unroll
@@ -943,8 +955,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         }
       };
       if (ok) {
-        give(TM_DQ, OFF_E, p.dq, DK, 64 * hf, 64);
-        give(TM_DK, OFF_P, p.dk, DK, 64 * hf, 64);
+        give(TM_DQ, OFF_E, p.dq, KD, KD / 2 * hf, KD / 2);
+        give(TM_DK, OFF_P, p.dk, KD, KD / 2 * hf, KD / 2);
         give(TM_DV, OFF_T, p.dv, DV, DV / 2 * hf, DV / 2);
       }
       fence_proxy_async_smem();
@@ -954,9 +966,9 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     if (!ok) break;
     if (lead && lane == 0 && len == C) {
       const int t = (int)t0;
-      for (int x = 0; x < DK; x += 64) {
-        tma_store_2d(&tm_dq, sb + OFF_E + 256 * x, h * DK + x, t);
-        tma_store_2d(&tm_dk, sb + OFF_P + 256 * x, h * DK + x, t);
+      for (int x = 0; x < KD; x += 64) {
+        tma_store_2d(&tm_dq, sb + OFF_E + 256 * x, h * KD + x, t);
+        tma_store_2d(&tm_dk, sb + OFF_P + 256 * x, h * KD + x, t);
       }
       for (int x = 0; x < DV; x += 64) tma_store_2d(&tm_dv, sb + OFF_T + 256 * x, h * DV + x, t);
       bulk_commit();
@@ -990,7 +1002,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 
 bool la_bwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen) {
   const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
-  return dtype == CKDA_BF16 && dk == la::bw::DK && (dv == 64 || dv == 128) && rows > 0 &&
+  return dtype == CKDA_BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) && rows > 0 &&
          rows <= 0x7fffffffull - la::bw::C && (uint64_t)H * (dk > dv ? dk : dv) <= 0x7fffffffull;
 }
 
@@ -998,7 +1010,7 @@ size_t la_bwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool 
                                  bool per_head) {
   const size_t slots = (size_t)la::chunk_slots(varlen, n_seqs, T, la::bw::C);
   const size_t tokens = varlen ? (size_t)T : (size_t)n_seqs * T;
-  return 2 * slots * H * dk * dv * 4 + (per_head ? (tokens * H * 4 + 255) / 256 * 256 : 0);
+  return 2 * slots * H * la::bw::state_floats(dv) * 4 + (per_head ? (tokens * H * 4 + 255) / 256 * 256 : 0);
 }
 
 cudaError_t launch_la_dalpha_sum(const float* part, float* da, int64_t tokens, int H,
@@ -1014,8 +1026,9 @@ cudaError_t launch_la_bwd_tc(int dk_, int dv_, const void* q, const void* k, con
   const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
   const int64_t slots = chunk_slots(varlen, n_seqs, T, bw::C);
   float* Sk = static_cast<float*>(ws);
-  float* Gk = Sk + (size_t)slots * H * dk_ * dv_;
-  float* part = per_head ? Gk + (size_t)slots * H * dk_ * dv_ : dalpha;
+  const size_t all = (size_t)slots * H * bw::state_floats(dv_);
+  float* Gk = Sk + all;
+  float* part = per_head ? Gk + all : dalpha;
   const Decay al{alpha, H, per_head};
   CUtensorMap mq, mk, mv, mo, nq, nk, nv;
   const uint64_t ck_ = (uint64_t)H * dk_, cv = (uint64_t)H * dv_;
@@ -1026,8 +1039,9 @@ cudaError_t launch_la_bwd_tc(int dk_, int dv_, const void* q, const void* k, con
     return cudaErrorInvalidValue;
   cudaError_t e;
   {
-    auto ks = bw::st::la_states_kernel;
-    if ((e = max_smem<10>(ks, bw::st::kSmem)) != cudaSuccess) return e;
+    auto ks = dk_ == 128 ? bw::st::la_states_kernel<128> : bw::st::la_states_kernel<64>;
+    e = dk_ == 128 ? max_smem<10>(ks, bw::st::kSmem) : max_smem<11>(ks, bw::st::kSmem);
+    if (e != cudaSuccess) return e;
     const bw::st::Args a{al, S0, dSf, Sk, Gk, dS0, cu, n_seqs, T, H, dv_, status};
     ks<<<(unsigned)n_seqs * H * 2 * (dv_ / bw::st::BV), bw::st::kThreads, bw::st::kSmem, stream>>>(
         mq, mk, mv, mo, a);
@@ -1047,16 +1061,20 @@ cudaError_t launch_la_bwd_tc(int dk_, int dv_, const void* q, const void* k, con
                        slots * H,
                        status};
   const unsigned grid = (unsigned)(a.units < 148 ? a.units : 148);
-  if (dv_ == 128) {
-    auto kc = bw::ck::la_chunk_kernel<128>;
-    if ((e = max_smem<11>(kc, bw::ck::kSmem)) != cudaSuccess) return e;
+  auto run = [&](auto kc, cudaError_t attr) -> cudaError_t {
+    if (attr != cudaSuccess) return attr;
     kc<<<grid, bw::ck::kThreads, bw::ck::kSmem, stream>>>(mq, mk, mv, mo, nq, nk, nv, a);
-  } else {
-    auto kc = bw::ck::la_chunk_kernel<64>;
-    if ((e = max_smem<12>(kc, bw::ck::kSmem)) != cudaSuccess) return e;
-    kc<<<grid, bw::ck::kThreads, bw::ck::kSmem, stream>>>(mq, mk, mv, mo, nq, nk, nv, a);
-  }
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return cudaGetLastError();
+  };
+#define CKDA_LA_CHUNK(KD, DV)                      \
+  run(bw::ck::la_chunk_kernel<KD, DV>,             \
+      max_smem<20 + KD + DV / 64>(bw::ck::la_chunk_kernel<KD, DV>, bw::ck::kSmem))
+  if (dk_ == 128)
+    e = dv_ == 128 ? CKDA_LA_CHUNK(128, 128) : CKDA_LA_CHUNK(128, 64);
+  else
+    e = dv_ == 128 ? CKDA_LA_CHUNK(64, 128) : CKDA_LA_CHUNK(64, 64);
+#undef CKDA_LA_CHUNK
+  if (e != cudaSuccess) return e;
   return per_head ? launch_la_dalpha_sum(part, dalpha, (int64_t)rows, H, stream) : cudaSuccess;
 }
 

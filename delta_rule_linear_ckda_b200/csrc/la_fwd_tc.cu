@@ -1,5 +1,5 @@
 // Head-decay linear attention on the tensor cores (tcgen05): bf16 inputs,
-// d_k = 128, d_v a multiple of 64 (sm_100a).
+// d_k 64 or 128, d_v a multiple of 64 (sm_100a).
 //
 // Per chunk of C = 128 tokens (start state S, D(i, j) = a_{j+1} .. a_i):
 //   O = (D o Q K^T) V + diag(pre) Q S,   S' = gamma S + K^T diag(suf) V,
@@ -51,7 +51,7 @@ using namespace sm100;
 namespace fw {
 
 constexpr int C = 128;
-constexpr int DK = 128;
+constexpr int DK = 128;  // rows of the state's product; those behind a d_k of 64 are zero
 constexpr int BV = 64;  // d_v columns per CTA
 constexpr uint64_t kWaitNs = 2000000000ull;  // 2 s per wait
 
@@ -115,7 +115,8 @@ struct Args {
 };
 
 // SUM: the pieces' own end states only (those of segments 0 .. seg_n - 2)
-template <typename Tout, bool SUM>
+// KD: d_k
+template <typename Tout, bool SUM, int KD>
 __global__ void __launch_bounds__(kThreads, 1)
 la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
               const __grid_constant__ CUtensorMap tm_v,
@@ -170,6 +171,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   if (warp == 0) {
     tmem_alloc(sb + OFF_MISC, kTmemCols);
     tmem_relinquish();
+  }
+  if constexpr (KD < DK) {  // no load writes K's second 64 columns
+    for (int e = tid; e < 2 * 16384 / 16; e += kThreads)
+      *reinterpret_cast<uint4*>(sm + OFF_K + (e >> 10) * 32768 + 16384 + (e & 1023) * 16) =
+          make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -328,7 +335,8 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     for (int e = 0; e < kHalf; ++e) S[e] = 0.f;
     const size_t unit = (size_t)n * p.H + h;
     const size_t at = ((size_t)r * p.DV) + j0 + kHalf * hf;  // this thread's columns of a state
-    const size_t stsz = (size_t)DK * p.DV;
+    const size_t stsz = (size_t)KD * p.DV;
+    const bool row_in = KD == DK || r < KD;
     float* part = p.part + unit * np * stsz + at;
     {
       // segment 0 starts from S0; with segments, from a copy of it that the
@@ -343,7 +351,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           src = SUM ? nullptr : part + g * stsz;
         else if (seg == 0 && p.S0 != nullptr)
           src = !SUM && p.seg_n > 1 ? part : p.S0 + unit * stsz + at;
-        if (src != nullptr) {
+        if (src != nullptr && row_in) {
 #pragma unroll
           for (int e = 0; e < kHalf; e += 4) {
             const float4 x = *reinterpret_cast<const float4*>(src + e);
@@ -355,7 +363,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         if (!SUM && g > 0) f *= p.dec[unit * np + g - 1];
       }
-      if (SUM && seg == 0 && p.S0 != nullptr) store_cols<kHalf>(part, S);
+      if (SUM && seg == 0 && p.S0 != nullptr && row_in) store_cols<kHalf>(part, S);
     }
     float gamma = 1.f, total = 1.f;
 #pragma unroll 1
@@ -429,9 +437,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
               *reinterpret_cast<uint4*>(sm + OFF_VW + e * 16384 + o) = z;
           }
 #pragma unroll 1
-          for (int c8 = 0; c8 < DK / 16; ++c8)
+          for (int c8 = 0; c8 < KD / 16; ++c8)
             *reinterpret_cast<uint4*>(sm + OFF_K + st * 32768 +
-                                      sw128_chunk(r, (DK / 2) * hf + 8 * c8, 128)) = z;
+                                      sw128_chunk(r, (KD / 2) * hf + 8 * c8, 128)) = z;
         }
       }
       fence_proxy_async_smem();
@@ -450,9 +458,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     }
     if (ok) {
       if (SUM) {
-        store_cols<kHalf>(part + (seg + 1) * stsz, S);
+        if (row_in) store_cols<kHalf>(part + (seg + 1) * stsz, S);
         if (r == 0 && hf == 0 && j0 == 0) p.dec[unit * np + seg] = total;
-      } else if (p.Sf != nullptr && seg == p.seg_n - 1) {
+      } else if (p.Sf != nullptr && seg == p.seg_n - 1 && row_in) {
         store_cols<kHalf>(p.Sf + unit * stsz + at, S);
       }
     }
@@ -473,7 +481,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const uint64_t so = (uint64_t)(c & 1) * (32768 >> 4);
       if (elect_one()) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
+        for (int kk = 0; kk < KD / 16; ++kk) {
           const uint64_t ko = so + 1024 * (kk >> 2) + 2 * (kk & 3);
           mma_f16(tmem + TM_SC, d_q + ko, d_k + ko, id_sc, kk > 0 ? 1u : 0u);
         }
@@ -504,7 +512,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
+          for (int kk = 0; kk < KD / 16; ++kk)
             mma_f16(tmem + TM_O1, d_q + so + 1024 * (kk >> 2) + 2 * (kk & 3), d_sb + 128 * kk,
                     id_qs, kk > 0 ? 1u : 0u);
           mma_commit(bar + B_QS + 8 * st);
@@ -545,16 +553,14 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       auto tok = [&](int c) { return (int)(tok0 + (int64_t)c * C); };
       auto load_q = [&](int c) {
         const uint32_t bq = bar + B_Q + 8 * (c & 1), dst = sb + OFF_Q + (c & 1) * 32768;
-        mbar_expect_tx(bq, 32768);
-        tma_load_2d(dst, &tm_q, h * DK, tok(c), bq);
-        tma_load_2d(dst + 16384, &tm_q, h * DK + 64, tok(c), bq);
+        mbar_expect_tx(bq, 256 * KD);
+        for (int x = 0; x < KD; x += 64) tma_load_2d(dst + 256 * x, &tm_q, h * KD + x, tok(c), bq);
         issued(0, c);
       };
       auto load_k = [&](int c) {
         const uint32_t bk = bar + B_K + 8 * (c & 1), dst = sb + OFF_K + (c & 1) * 32768;
-        mbar_expect_tx(bk, 32768);
-        tma_load_2d(dst, &tm_k, h * DK, tok(c), bk);
-        tma_load_2d(dst + 16384, &tm_k, h * DK + 64, tok(c), bk);
+        mbar_expect_tx(bk, 256 * KD);
+        for (int x = 0; x < KD; x += 64) tma_load_2d(dst + 256 * x, &tm_k, h * KD + x, tok(c), bk);
         issued(1, c);
       };
       auto load_v = [&](int c) {
@@ -566,9 +572,9 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // into L2 two chunks ahead of the loads
       auto prefetch = [&](int c) {
         if (c >= nck) return;
-        for (int x = 0; x < 128; x += 64) {
-          if (!SUM) tma_prefetch_2d(&tm_q, h * DK + x, tok(c));
-          tma_prefetch_2d(&tm_k, h * DK + x, tok(c));
+        for (int x = 0; x < KD; x += 64) {
+          if (!SUM) tma_prefetch_2d(&tm_q, h * KD + x, tok(c));
+          tma_prefetch_2d(&tm_k, h * KD + x, tok(c));
         }
         tma_prefetch_2d(&tm_v, h * p.DV + j0, tok(c));
       };
@@ -664,7 +670,7 @@ static int fwd_pieces(int n_seqs, int H, int dv, int segs) {
 
 bool la_fwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen) {
   const uint64_t rows = varlen ? (uint64_t)T : (uint64_t)n_seqs * (uint64_t)T;
-  return dtype == CKDA_BF16 && dk == la::fw::DK && (dv == 64 || dv == 128) && rows > 0 &&
+  return dtype == CKDA_BF16 && (dk == 64 || dk == 128) && (dv == 64 || dv == 128) && rows > 0 &&
          rows <= 0x7fffffffull - la::fw::C &&
          (uint64_t)H * (dk > dv ? dk : dv) <= 0x7fffffffull;
 }
@@ -674,6 +680,33 @@ size_t la_fwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool 
   const int np = g * la::fwd_pieces(n_seqs, H, dv, g);
   return g > 1 ? (size_t)n_seqs * H * np * ((size_t)dk * dv + 64) * 4 : 0;
 }
+
+namespace la {
+
+template <int KD>
+static cudaError_t fwd_run(int out_dtype, unsigned units, fw::Args a, const CUtensorMap& mq,
+                           const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mo,
+                           cudaStream_t stream) {
+  cudaError_t e;
+  if (a.seg_n > 1) {
+    auto ks = fw::la_fwd_kernel<float, true, KD>;
+    if ((e = max_smem<KD>(ks, fw::kSmem)) != cudaSuccess) return e;
+    ks<<<units * (a.seg_n - 1) * a.piece_n, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  if (out_dtype == CKDA_BF16) {
+    auto kb = fw::la_fwd_kernel<__nv_bfloat16, false, KD>;
+    if ((e = max_smem<KD + 1>(kb, fw::kSmem)) != cudaSuccess) return e;
+    kb<<<units * a.seg_n, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
+  } else {
+    auto kf = fw::la_fwd_kernel<float, false, KD>;
+    if ((e = max_smem<KD + 2>(kf, fw::kSmem)) != cudaSuccess) return e;
+    kf<<<units * a.seg_n, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace la
 
 cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const void* k,
                              const void* v, const float* alpha, int per_head, const float* S0,
@@ -695,25 +728,12 @@ cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const
   fw::Args a{{alpha, H, per_head}, S0, cu, out, S_final, n_seqs, T, H, dv, status, g, np / g,
              nullptr, nullptr};
   const unsigned units = (unsigned)n_seqs * H * (dv / fw::BV);
-  cudaError_t e;
   if (g > 1) {
     a.part = static_cast<float*>(ws);
     a.dec = a.part + (size_t)n_seqs * H * np * dk * dv;
-    auto ks = fw::la_fwd_kernel<float, true>;
-    if ((e = max_smem<0>(ks, fw::kSmem)) != cudaSuccess) return e;
-    ks<<<units * (np - np / g), fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
-  if (out_dtype == CKDA_BF16) {
-    auto kb = fw::la_fwd_kernel<__nv_bfloat16, false>;
-    if ((e = max_smem<1>(kb, fw::kSmem)) != cudaSuccess) return e;
-    kb<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
-  } else {
-    auto kf = fw::la_fwd_kernel<float, false>;
-    if ((e = max_smem<2>(kf, fw::kSmem)) != cudaSuccess) return e;
-    kf<<<units * g, fw::kThreads, fw::kSmem, stream>>>(mq, mk, mv, mo, a);
-  }
-  return cudaGetLastError();
+  return dk == 128 ? fwd_run<128>(out_dtype, units, a, mq, mk, mv, mo, stream)
+                   : fwd_run<64>(out_dtype, units, a, mq, mk, mv, mo, stream);
 }
 
 }  // namespace ckda

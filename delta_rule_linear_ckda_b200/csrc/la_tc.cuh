@@ -55,23 +55,25 @@ __device__ __forceinline__ T warp_suffix(T a, int lane) {
 }
 
 // A chunk's decays (four blocks of 32 tokens, a lane one of each) for the other
-// warps: {a[128], sufW[128], tot[4], gamma}.  The products are taken in 64 bits
-// and rounded once: in 32 bits their errors all lie on one side when the decay
-// is the same for every token, and add up over a long state (1e-6 of S_final
-// after 4096 tokens instead of 2e-7).
+// warps: {a[128], sufW[128], tot[4], gamma}.  gamma, whose error the state
+// takes on again with every chunk, is multiplied up in 64 bits and rounded
+// once: in 32 bits the errors all lie on one side when the decay is the same
+// for every token (1e-6 of S_final after 4096 tokens instead of 2e-7).  The
+// others stay in 32 bits: 64-bit shuffles for all of them cost a tenth of the
+// forward's time, which shared memory bounds.
 constexpr int kDecFloats = 264;
 __device__ __forceinline__ void put_decays(float* o, const float* a, int lane) {
-  double all = 1.0;
+  double all = ((double)a[0] * (double)a[1]) * ((double)a[2] * (double)a[3]);
+#pragma unroll
+  for (int d = 16; d >= 1; d >>= 1) all *= __shfl_xor_sync(0xffffffffu, all, d);
 #pragma unroll
   for (int bk = 0; bk < 4; ++bk) {
-    const double x = (double)a[bk];
-    const double pw = warp_prefix(x, lane), sw = warp_suffix(x, lane);
+    const float pw = warp_prefix(a[bk], lane), sw = warp_suffix(a[bk], lane);
     o[32 * bk + lane] = a[bk];
-    o[128 + 32 * bk + lane] = (float)sw;
-    if (lane == 31) o[256 + bk] = (float)pw;
-    all *= pw;
+    o[128 + 32 * bk + lane] = sw;
+    if (lane == 31) o[256 + bk] = pw;
   }
-  if (lane == 31) o[260] = (float)all;
+  if (lane == 0) o[260] = (float)all;
 }
 
 __device__ __forceinline__ float lo_f(uint32_t x) { return __uint_as_float(x << 16); }

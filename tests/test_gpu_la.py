@@ -21,7 +21,7 @@ def ck():
 
 
 def tensor_core(ck, dk, dv, dtype):
-    return dtype == torch.bfloat16 and dk == 128 and dv in (64, 128)
+    return dtype == torch.bfloat16 and dk in (64, 128) and dv in (64, 128)
 
 
 def make(lead, H, dk, dv, dtype, decay="token", seed=0, n=None, states=True):
@@ -91,7 +91,7 @@ def test_backward_head_sizes(ck, dk, dv, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("decay", ["zeros", "head"])
-@pytest.mark.parametrize("dk,dv", [(128, 128), (32, 16)])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (32, 16)])
 def test_packed(ck, dk, dv, decay, dtype):
     lens = [70, 0, 129, 1, 64, 5, 0, 300, 128, 0]
     cu = torch.tensor([0] + lens, device=DEV).cumsum(0).to(torch.int32)
@@ -163,13 +163,13 @@ def test_step(ck, dk, dv, B, H, dtype):
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 def test_few_heads_and_long_sequences(ck, dtype):
     """Lengths that a tensor-core call splits into segments; S_final over S0."""
-    for B, T, H, dv, lens in ((1, 4500, 2, 128, None), (2, 2200, 1, 64, None),
-                              (3, 5000, 1, 128, [1, 4980, 19])):
+    for B, T, H, dk, dv, lens in ((1, 4500, 2, 128, 128, None), (2, 2200, 1, 64, 64, None),
+                                  (3, 5000, 1, 128, 128, [1, 4980, 19])):
         lead, cu = (B, T), None
         if lens:
             lead, cu = (T,), torch.tensor([0] + lens, device=DEV).cumsum(0).to(torch.int32)
         for decay in ("signed", "one"):
-            q, k, v, a, _, S0, _ = make(lead, H, 128, dv, dtype, decay, seed=T, n=B)
+            q, k, v, a, _, S0, _ = make(lead, H, dk, dv, dtype, decay, seed=T, n=B)
             check_fwd(ck, q, k, v, a, S0, cu)
             o, S = ck.la_fwd_chunked(q, k, v, a, S0=S0, cu_seqlens=cu)
             Sio = S0.clone()
