@@ -470,9 +470,8 @@ CKDA_API int ckda_sfda_decode_step(const void* q, const void* k, const void* v,
  *
  *     S_t = a_t S_{t-1} + k_t v_t^T,   o_t = S_t^T q_t,   a_t in [-1, 1].
  *
- * ("Understanding Kimi Delta Attention and its Extensions": the gated linear
- * recurrence that the delta rule extends; it is the Gated DeltaNet-2 form
- * with the erase gate 0, the write gate 1 and a scalar decay.)  Products of
+ * It is the Gated DeltaNet-2 recurrence with the erase gate 0, the write gate
+ * 1 and a scalar decay; the pages give it no section of its own.  Products of
  * decays are running products, never quotients or logarithms: zero and
  * negative decays are exact.  Rules as for ckda_fwd_chunked, and:
  *
@@ -487,10 +486,11 @@ CKDA_API int ckda_sfda_decode_step(const void* q, const void* k, const void* v,
  *                   aligned, overlapping no tensor; calls that may run at
  *                   the same time need workspaces of their own.  The query
  *                   may return 0, workspace may then be NULL.
- * Tokens behind cu_seqlens' last offset are neither read nor written.  With
- * bf16 inputs and d_k, d_v large enough for the tensor cores the products'
- * operands are bf16, their sums fp32, and a row of out is within a few bf16
- * roundings of the exact one; S_final keeps fp32 accuracy.
+ * bf16 inputs with d_k, d_v in {64, 128} run on the tensor cores: the scores
+ * (times their decays) and the copy of the state that the queries read are
+ * rounded to bf16 once each, all sums are fp32, and S_final keeps fp32
+ * accuracy.  A value that is not finite in a sequence reaches that sequence's
+ * outputs only.
  */
 CKDA_API int ckda_la_fwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
                                  const float* S0, const int32_t* cu_seqlens, void* out,
@@ -507,8 +507,9 @@ CKDA_API int64_t ckda_la_fwd_workspace_bytes(int B, int T, int H, int d_k, int d
  * and typed like q, k, v; dalpha (fp32) is shaped like alpha, summed over the
  * tokens when alpha_per_head is 1; dS0 (fp32) may be NULL.  The gradient of a
  * zero decay is that of the recurrence (no division by a_t).  No output may
- * overlap another tensor.  Every output element is written by every call
- * (tokens behind the last sequence excepted), sums are in a fixed order.
+ * overlap another tensor.  Every output element is written by every call, sums
+ * are in a fixed order: the same call gives the same bits.  dalpha and dS0
+ * keep fp32 accuracy with bf16 inputs too.
  */
 CKDA_API int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
                                  const float* S0, const int32_t* cu_seqlens, const void* dO,
