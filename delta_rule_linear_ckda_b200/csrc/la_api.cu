@@ -23,6 +23,8 @@ cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const
 cudaError_t launch_la_decode(int dtype, int out_dtype, int dk, int dv, const void* q, const void* k,
                              const void* v, const float* alpha, int per_head, float* S, void* out,
                              int B, int H, cudaStream_t stream);
+cudaError_t launch_la_dalpha_sum(const float* part, float* da, int64_t tokens, int H,
+                                 cudaStream_t stream);
 size_t la_bwd_simt_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen,
                                    bool per_head);
 cudaError_t launch_la_bwd_simt(int dtype, int dk_, int dv_, const void* q, const void* k,
@@ -178,12 +180,17 @@ int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float
   const int64_t tokens = varlen ? (int64_t)T : (int64_t)B * T;
   if (tokens > 0 && (!q || !k || !v || !alpha || !dO || !dq || !dk || !dv || !dalpha))
     return CKDA_ERR_INVALID_ARG;
-  if (B > 0 && alpha_per_head && !dalpha) return CKDA_ERR_INVALID_ARG;  // [H], whatever T
+  if (alpha_per_head && !dalpha) return CKDA_ERR_INVALID_ARG;  // [H], whatever B and T
   const void* ptrs[] = {q, k, v, alpha, S0, dO, dS_final, dq, dk, dv, dalpha, dS0};
   for (const void* p : ptrs)
     if (!aligned16(p)) return CKDA_ERR_MISALIGNED;
   if ((reinterpret_cast<uintptr_t>(cu_seqlens) & 3u) != 0) return CKDA_ERR_MISALIGNED;
-  if (B == 0) return CKDA_OK;
+  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
+  if (B == 0) {  // a gradient of [H] is zero without a sequence too
+    if (!alpha_per_head) return CKDA_OK;
+    return ckda::launch_la_dalpha_sum(nullptr, dalpha, 0, H, st_) == cudaSuccess ? CKDA_OK
+                                                                                 : CKDA_ERR_CUDA;
+  }
   const size_t e = dtype == CKDA_BF16 ? 2 : 4;
   const size_t th = (size_t)tokens * H, st = (size_t)B * H * d_k * d_v * 4;
   const size_t al = (alpha_per_head ? (size_t)H : th) * 4;
@@ -202,7 +209,6 @@ int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float
   if (rc != CKDA_OK) return rc;
   int* status = ckda::status_word();
   if (status == nullptr) return CKDA_ERR_CUDA;
-  const cudaStream_t st_ = static_cast<cudaStream_t>(stream);
   const cudaError_t err =
       ckda::la_bwd_tc_supported(dtype, d_k, d_v, B, T, H, varlen)
           ? ckda::launch_la_bwd_tc(d_k, d_v, q, k, v, alpha, alpha_per_head, S0, cu_seqlens, dO,

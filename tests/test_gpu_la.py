@@ -280,6 +280,16 @@ def test_empty_calls(ck):
     assert torch.equal(ck.la_bwd_chunked(q, k, v, a, dO, S0=S0)["dalpha"], torch.zeros_like(a))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_no_sequence_leaves_a_zero_gradient_per_head(ck, dtype):
+    q, k, v, a, dO, S0, _ = make((0, 5), 2, 128, 128, dtype, "head")
+    cu = torch.zeros(1, dtype=torch.int32, device=DEV)
+    for args, c in (((q, k, v, a, dO), None), ((q[:, 0], k[:, 0], v[:, 0], a, dO[:, 0]), cu)):
+        g = {"dalpha": torch.full_like(a, float("nan"))}
+        ck.la_bwd_chunked(*args, S0=S0, cu_seqlens=c, grads=g)
+        assert torch.equal(g["dalpha"], torch.zeros_like(a))
+
+
 def test_bad_offsets_are_reported(ck):
     q, k, v, a, dO, _, _ = make((200,), 2, 128, 128, torch.bfloat16, states=False)
     for cu in ([0, 120, 90, 200], [0, 100, 180], [5, 100, 200], [0, 300, 200]):
