@@ -299,12 +299,19 @@ __global__ void __launch_bounds__(kThreads) bwd_kernel(const Args p) {
           dot += __shfl_xor_sync(0xffffffffu, dot, o);
         }
         const float r = inv_norm(ss, p);
-        const float m = p.c * r * r * r * dot;
+        // c r^3 x dot as products of x r and r dot, which stay in range where
+        // r^3 does not (rows below 1e-13 without an eps)
+        const float m = p.c * r * (r * dot);
+#pragma unroll
+        for (int i = 0; i < G; ++i) {
+          x[i] *= r;
+          y[i] *= r;
+        }
         if constexpr (SUMS) {  // (a lane without a row adds zeros)
 #pragma unroll
           for (int i = 0; i < G; ++i) {
-            dw[i] = fmaf(u[i], x[i] * r, dw[i]);
-            dw[G + i] = fmaf(v[i], y[i] * r, dw[G + i]);
+            dw[i] = fmaf(u[i], x[i], dw[i]);
+            dw[G + i] = fmaf(v[i], y[i], dw[G + i]);
           }
         }
 #pragma unroll

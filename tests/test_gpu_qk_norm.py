@@ -129,6 +129,13 @@ def test_rows_of_zeros_and_tiny_rows(ck):
     assert torch.equal(g["dq"][1], torch.zeros_like(o[1]))
 
 
+@pytest.mark.parametrize("norm", ["l2", "rms"])
+def test_small_rows_without_eps(ck, norm):
+    """r = |x|^-1 of these rows is in range, its third power is not."""
+    q, k, gq, gk, c = make(12, 2, 2, 64, 64, torch.float32, seed=16)
+    check(ck, (q * 1e-15, k * 1e-14, gq, gk, c), norm, eps=0.0)
+
+
 def test_a_row_that_is_not_finite_stays_alone(ck):
     q, k, gq, gk, c = make(33, 3, 3, 32, 32, torch.bfloat16, seed=7)
     ref = ck.qk_norm_rope(q, k, **c)
