@@ -477,18 +477,29 @@ __global__ void __launch_bounds__(kDaThreads) la_dalpha_kernel(const DalphaArgs 
 }
 
 // da[h] = the sum over the tokens of per-token gradients [tokens, H]: one CTA
-// per head, a fixed order, sums in 64 bits.
-__global__ void __launch_bounds__(256) la_dalpha_sum_kernel(const float* __restrict__ part,
-                                                            float* __restrict__ da, int64_t tokens,
-                                                            int H) {
-  __shared__ double red[256];
+// per head, a fixed order, sums in 64 bits.  A thread has eight loads on their
+// way at a time: a head's sum is a chain of latencies, not of bytes.
+constexpr int kSumThreads = 1024;
+__global__ void __launch_bounds__(kSumThreads) la_dalpha_sum_kernel(const float* __restrict__ part,
+                                                                    float* __restrict__ da,
+                                                                    int64_t tokens, int H) {
+  __shared__ double red[kSumThreads];
   const int h = blockIdx.x;
   double s = 0.0;
-  for (int64_t t = threadIdx.x; t < tokens; t += 256) s += (double)part[t * H + h];
+  for (int64_t t = threadIdx.x; t < tokens; t += 8 * kSumThreads) {
+    float x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int64_t at = t + e * kSumThreads;
+      x[e] = at < tokens ? __ldg(part + at * H + h) : 0.f;
+    }
+    s += (((double)x[0] + (double)x[1]) + ((double)x[2] + (double)x[3])) +
+         (((double)x[4] + (double)x[5]) + ((double)x[6] + (double)x[7]));
+  }
   red[threadIdx.x] = s;
   __syncthreads();
 #pragma unroll
-  for (int w = 128; w >= 1; w >>= 1) {
+  for (int w = kSumThreads / 2; w >= 1; w >>= 1) {
     if (threadIdx.x < w) red[threadIdx.x] += red[threadIdx.x + w];
     __syncthreads();
   }
@@ -508,7 +519,7 @@ cudaError_t launch_la_fwd_simt(int dtype, int out_dtype, int dk, int dv, const v
 
 cudaError_t launch_la_dalpha_sum(const float* part, float* da, int64_t tokens, int H,
                                  cudaStream_t stream) {
-  la::la_dalpha_sum_kernel<<<H, 256, 0, stream>>>(part, da, tokens, H);
+  la::la_dalpha_sum_kernel<<<H, la::kSumThreads, 0, stream>>>(part, da, tokens, H);
   return cudaGetLastError();
 }
 
