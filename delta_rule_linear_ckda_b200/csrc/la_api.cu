@@ -13,7 +13,9 @@ int* status_word();
 cudaError_t launch_la_fwd_simt(int dtype, int out_dtype, int dk, int dv, const void* q,
                                const void* k, const void* v, const float* alpha, int per_head,
                                const float* S0, const int32_t* cu, void* out, float* S_final,
-                               int n_seqs, int T, int H, int* status, cudaStream_t stream);
+                               void* ws, int n_seqs, int T, int H, int* status,
+                               cudaStream_t stream);
+size_t la_fwd_simt_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen);
 bool la_fwd_tc_supported(int dtype, int dk, int dv, int n_seqs, int T, int H, bool varlen);
 size_t la_fwd_tc_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen);
 cudaError_t launch_la_fwd_tc(int out_dtype, int dk, int dv, const void* q, const void* k,
@@ -108,8 +110,11 @@ extern "C" {
 int64_t ckda_la_fwd_workspace_bytes(int B, int T, int H, int d_k, int d_v, int dtype, int varlen) {
   const int rc = la_sizes(B, T, H, d_k, d_v, 0, dtype, varlen != 0);
   if (rc != CKDA_OK) return rc;
-  if (B == 0 || !ckda::la_fwd_tc_supported(dtype, d_k, d_v, B, T, H, varlen != 0)) return 0;
-  return (int64_t)ckda::la_fwd_tc_workspace_bytes(d_k, d_v, B, T, H, varlen != 0);
+  if (B == 0) return 0;
+  const bool vl = varlen != 0;
+  return (int64_t)(ckda::la_fwd_tc_supported(dtype, d_k, d_v, B, T, H, vl)
+                       ? ckda::la_fwd_tc_workspace_bytes(d_k, d_v, B, T, H, vl)
+                       : ckda::la_fwd_simt_workspace_bytes(d_k, d_v, B, T, H, vl));
 }
 
 int ckda_la_fwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
@@ -154,7 +159,7 @@ int ckda_la_fwd_chunked(const void* q, const void* k, const void* v, const float
           ? ckda::launch_la_fwd_tc(out_dtype, d_k, d_v, q, k, v, alpha, alpha_per_head, S0,
                                    cu_seqlens, out, S_final, workspace, B, T, H, status, st_)
           : ckda::launch_la_fwd_simt(dtype, out_dtype, d_k, d_v, q, k, v, alpha, alpha_per_head, S0,
-                                     cu_seqlens, out, S_final, B, T, H, status, st_);
+                                     cu_seqlens, out, S_final, workspace, B, T, H, status, st_);
   return err == cudaSuccess ? CKDA_OK : CKDA_ERR_CUDA;
 }
 

@@ -20,6 +20,12 @@
 // Tokens come 16 at a time through shared memory, the next 16 already on
 // their way in registers; the row groups' shares of the outputs are summed
 // once per 16 tokens, so no barrier stands between tokens.
+//
+// A recurrence of few heads leaves most SMs empty and takes as long as its
+// tokens take one after another.  Its sequences are then split into segments
+// of whole chunks that run at the same time: a first launch carries each
+// segment's own state to its end (keys and values only), the second starts
+// every segment from their decayed sum.
 #include "la_common.cuh"
 
 namespace ckda {
@@ -44,6 +50,13 @@ struct RecArgs {
   const int32_t* cu;
   int n_seqs, T, H, DV;
   int* status;
+  // segments per sequence, numbered in the order of the recurrence;
+  // part[(n H + h) seg_n + g], [DK, DV]: for g > 0 the end state of segment
+  // g - 1 (segment 0's from X0, the others' from zero), for g = 0 a copy of
+  // X0; dec: the segments' decays
+  int seg_n;
+  float* part;
+  float* dec;
 };
 
 template <int DK, int COLS>
@@ -52,7 +65,8 @@ struct RecSmem {
   float red[kTile][kRecThreads / COLS][COLS];
 };
 
-template <int DK, int COLS, typename Tin, typename Tout, bool REV>
+// SUM: the segments' own end states only (all but the last segment)
+template <int DK, int COLS, typename Tin, typename Tout, bool REV, bool SUM>
 __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSmem<DK, COLS>& sm) {
   constexpr int RG = kRecThreads / COLS;  // row groups
   constexpr int RPT = DK / RG;            // rows per thread
@@ -67,30 +81,71 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
 
   const int tid = threadIdx.x;
   const int col = tid % COLS, g = tid / COLS;
-  // block index: column slice, then head, then sequence (longest first)
-  const int slices = p.DV / COLS;
+  // block index: column slice, then segment, then head, then sequence (longest first)
+  const int slices = p.DV / COLS, nseg = SUM ? p.seg_n - 1 : p.seg_n;
   const int j0 = (int)(block % slices) * COLS;
-  const int h = (int)(block / slices % p.H);
-  const int n = seq_longest_first(p.cu, p.n_seqs, (int)(block / slices / p.H));
+  block /= slices;
+  const int seg = (int)(block % nseg);
+  block /= nseg;
+  const int h = (int)(block % p.H);
+  const int n = seq_longest_first(p.cu, p.n_seqs, (int)(block / p.H));
   const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
   if (!sr.ok) return;
   const int len = (int)(sr.end - sr.begin);
   const int ntiles = (len + kTile - 1) / kTile;
+  constexpr int per = kChunk / kTile;
+  // this segment's tiles [tb, te)
+  int tb = 0, te = ntiles;
+  if (p.seg_n > 1) {
+    const int64_t nck = (len + kChunk - 1) / kChunk;
+    const int g = REV ? p.seg_n - 1 - seg : seg;
+    tb = (int)(g * nck / p.seg_n) * per;
+    te = min(ntiles, (int)((g + 1) * nck / p.seg_n) * per);
+  }
   const Tin* q = static_cast<const Tin*>(p.q);
   const Tin* k = static_cast<const Tin*>(p.k);
   const Tin* v = static_cast<const Tin*>(p.v);
 
-  const size_t st0 = ((size_t)n * p.H + h) * DK * p.DV;
+  const size_t unit = (size_t)n * p.H + h, st0 = unit * DK * p.DV;
   const int i0 = g * RPT;
+  // this thread's column of part's states
+  float* part = p.part + unit * p.seg_n * DK * p.DV + (size_t)i0 * p.DV + j0 + col;
+  auto put_part = [&](int at, const float2* x) {
+    float* o = part + (size_t)at * DK * p.DV;
+#pragma unroll
+    for (int r = 0; r < RPT / 2; ++r) {
+      o[(size_t)(2 * r) * p.DV] = x[r].x;
+      o[(size_t)(2 * r + 1) * p.DV] = x[r].y;
+    }
+  };
   float2 X[RPT / 2];
 #pragma unroll
-  for (int r = 0; r < RPT / 2; ++r) {
-    X[r] = make_float2(0.f, 0.f);
-    if (p.X0 != nullptr) {
-      const float* b = p.X0 + st0 + (size_t)(j0 + col) * p.sj;
+  for (int r = 0; r < RPT / 2; ++r) X[r] = make_float2(0.f, 0.f);
+  if (p.X0 != nullptr && (SUM ? seg == 0 : p.seg_n == 1)) {
+    const float* b = p.X0 + st0 + (size_t)(j0 + col) * p.sj;
+#pragma unroll
+    for (int r = 0; r < RPT / 2; ++r)
       X[r] = make_float2(b[(size_t)(i0 + 2 * r) * p.si], b[(size_t)(i0 + 2 * r + 1) * p.si]);
+    // (the second launch starts from a copy: its last segment may write Xf
+    // over X0 before its first one starts)
+    if constexpr (SUM) put_part(0, X);
+  }
+  if (!SUM && p.seg_n > 1) {
+    float f = 1.f;
+#pragma unroll 1
+    for (int e = seg; e >= 0; --e) {
+      if (e > 0 || (seg == 0 && p.X0 != nullptr)) {
+        const float* b = part + (size_t)e * DK * p.DV;
+        const float2 f2 = make_float2(f, f);
+#pragma unroll
+        for (int r = 0; r < RPT / 2; ++r)
+          X[r] = fma2(f2, make_float2(b[(size_t)(2 * r) * p.DV], b[(size_t)(2 * r + 1) * p.DV]),
+                      X[r]);
+      }
+      if (e > 0) f *= p.dec[unit * p.seg_n + e - 1];
     }
   }
+  double total = 1.0;  // SUM: this thread's share of the segment's decay
 
   float rq[LQ], rk[LQ], rv[LV], ra = 0.f;
   // the tile's rows past the sequence's end are zero, so that what lies
@@ -102,7 +157,7 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
     for (int e = 0; e < LQ; ++e) {
       const int x = tid + e * kRecThreads, t = x / DK, i = x % DK;
       const size_t at = ((size_t)(t0 + t) * p.H + h) * DK + i;
-      rq[e] = t < rows ? Elem<Tin>::to_f32(q[at]) : 0.f;
+      if constexpr (!SUM) rq[e] = t < rows ? Elem<Tin>::to_f32(q[at]) : 0.f;
       rk[e] = t < rows ? Elem<Tin>::to_f32(k[at]) : 0.f;
     }
 #pragma unroll
@@ -114,16 +169,17 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
   };
 
   const int64_t slot0 = p.kept != nullptr ? slot_of(p.cu, n, p.T, kChunk) : 0;
-  if (ntiles > 0) fetch(REV ? ntiles - 1 : 0);
-  for (int it = 0; it < ntiles; ++it) {
-    const int tl = REV ? ntiles - 1 - it : it;
+  const int mine = te - tb;
+  if (mine > 0) fetch(REV ? te - 1 : tb);
+  for (int it = 0; it < mine; ++it) {
+    const int tl = REV ? te - 1 - it : tb + it;
     const int64_t t0 = sr.begin + (int64_t)tl * kTile;
     const int rows = min(kTile, len - tl * kTile);
     __syncthreads();  // the last tile's reads are done
 #pragma unroll
     for (int e = 0; e < LQ; ++e) {
       const int x = tid + e * kRecThreads;
-      sq[x / DK][x % DK] = rq[e];
+      if constexpr (!SUM) sq[x / DK][x % DK] = rq[e];
       sk[x / DK][x % DK] = rk[e];
     }
 #pragma unroll
@@ -131,12 +187,14 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
       const int x = tid + e * kRecThreads;
       sv[x / COLS][x % COLS] = rv[e];
     }
-    if (tid < kTile) sa[tid] = ra;
+    if (tid < kTile) {
+      sa[tid] = ra;
+      if constexpr (SUM) total *= (double)ra;
+    }
     __syncthreads();
-    if (it + 1 < ntiles) fetch(REV ? tl - 1 : tl + 1);
+    if (it + 1 < mine) fetch(REV ? tl - 1 : tl + 1);
 
-    constexpr int per = kChunk / kTile;
-    if (p.kept != nullptr && (REV ? (tl % per == per - 1 || tl == ntiles - 1) : tl % per == 0)) {
+    if (!SUM && p.kept != nullptr && (REV ? (tl % per == per - 1 || tl == ntiles - 1) : tl % per == 0)) {
       float* o = p.kept + ((size_t)(slot0 + tl / per) * p.H + h) * DK * p.DV + j0 + col;
 #pragma unroll
       for (int r = 0; r < RPT / 2; ++r) {
@@ -155,14 +213,15 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
 #pragma unroll
       for (int r = 0; r < RPT / 2; ++r) {
         const float2 k2 = *reinterpret_cast<const float2*>(&sk[t][i0 + 2 * r]);
-        const float2 q2 = *reinterpret_cast<const float2*>(&sq[t][i0 + 2 * r]);
         X[r] = fma2(X[r], a2, mul2(k2, v2));
+        if constexpr (SUM) continue;
+        const float2 q2 = *reinterpret_cast<const float2*>(&sq[t][i0 + 2 * r]);
         if (r & 1)
           o1 = fma2(q2, X[r], o1);
         else
           o = fma2(q2, X[r], o);
       }
-      red[t][g][col] = (o.x + o1.x) + (o.y + o1.y);
+      if constexpr (!SUM) red[t][g][col] = (o.x + o1.x) + (o.y + o1.y);
     };
     if (rows == kTile) {
 #pragma unroll 4
@@ -182,6 +241,7 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
 #pragma unroll
       for (int r = 0; r < RPT / 2; ++r) X[r] = mul2(X[r], a2);
     }
+    if constexpr (SUM) continue;
     __syncthreads();
     if (p.out != nullptr) {
       Tout* out = static_cast<Tout*>(p.out);
@@ -197,7 +257,15 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
       }
     }
   }
-  if (p.Xf != nullptr) {
+  if constexpr (SUM) {
+    put_part(seg + 1, X);
+    if (tid < kTile) {
+#pragma unroll
+      for (int o = kTile / 2; o >= 1; o >>= 1)
+        total *= __shfl_xor_sync(0xffffffffu >> (32 - kTile), total, o);
+      if (tid == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = (float)total;
+    }
+  } else if (p.Xf != nullptr && seg == p.seg_n - 1) {
     float* b = p.Xf + st0 + (size_t)(j0 + col) * p.sj;
 #pragma unroll
     for (int r = 0; r < RPT / 2; ++r) {
@@ -207,10 +275,10 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
   }
 }
 
-template <int DK, int COLS, typename Tin, typename Tout, bool REV>
-__global__ void __launch_bounds__(kRecThreads) la_rec_kernel(const RecArgs p) {
+template <int DK, int COLS, typename Tin, typename Tout, bool REV, bool SUM>
+__global__ void __launch_bounds__(kRecThreads, 4) la_rec_kernel(const RecArgs p) {
   __shared__ __align__(16) RecSmem<DK, COLS> sm;
-  rec_body<DK, COLS, Tin, Tout, REV>(p, blockIdx.x, sm);
+  rec_body<DK, COLS, Tin, Tout, REV, SUM>(p, blockIdx.x, sm);
 }
 
 // The backward's three recurrences at once, when d_k = d_v: they do not depend
@@ -220,38 +288,79 @@ struct Rec3Args {
   RecArgs fwd, rev[2];
 };
 
-template <int DK, int COLS, typename T>
-__global__ void __launch_bounds__(kRecThreads) la_rec3_kernel(const Rec3Args p) {
+template <int DK, int COLS, typename T, bool SUM>
+__global__ void __launch_bounds__(kRecThreads, 4) la_rec3_kernel(const Rec3Args p) {
   __shared__ __align__(16) RecSmem<DK, COLS> sm;
   const unsigned which = blockIdx.x % 3, block = blockIdx.x / 3;
   if (which == 0)
-    rec_body<DK, COLS, T, T, false>(p.fwd, block, sm);
+    rec_body<DK, COLS, T, T, false, SUM>(p.fwd, block, sm);
   else
-    rec_body<DK, COLS, T, T, true>(p.rev[which - 1], block, sm);
+    rec_body<DK, COLS, T, T, true, SUM>(p.rev[which - 1], block, sm);
+}
+
+constexpr int rec_columns(int dv) { return dv == 16 ? 16 : 32; }
+
+// Segments per sequence of recurrences with `dv` columns that run together:
+// as many as give every SM four CTAs, if each keeps two chunks.
+static int rec_segments(int together, int n_seqs, int T, int H, int dv, bool varlen) {
+  const int64_t ctas = (int64_t)together * n_seqs * H * (dv / rec_columns(dv));
+  int64_t g = 148 * 4 / (ctas > 0 ? ctas : 1);
+  const int64_t most = (int64_t)T / (n_seqs > 0 && varlen ? n_seqs : 1) / (2 * kChunk);
+  if (g > most) g = most;
+  return g < 2 ? 1 : (int)g;
+}
+
+// Floats of the segments' states and decays.
+static size_t part_floats(int dk, int dv, int n_seqs, int H, int seg_n) {
+  return seg_n > 1 ? (size_t)n_seqs * H * seg_n * ((size_t)dk * dv + 64) : 0;
+}
+
+static void set_parts(RecArgs* a, int dk, int seg_n, float* ws) {
+  a->seg_n = seg_n;
+  a->part = ws;
+  a->dec = seg_n > 1 ? ws + (size_t)a->n_seqs * a->H * seg_n * dk * a->DV : nullptr;
+}
+
+template <int DK, int COLS, typename T>
+static cudaError_t rec3_launch(const Rec3Args& a, cudaStream_t st) {
+  const RecArgs& f = a.fwd;
+  const unsigned n = 3u * (unsigned)(f.DV / COLS) * f.H * f.n_seqs;
+  if (f.seg_n > 1) {
+    la_rec3_kernel<DK, COLS, T, true><<<n * (f.seg_n - 1), kRecThreads, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  la_rec3_kernel<DK, COLS, T, false><<<n * f.seg_n, kRecThreads, 0, st>>>(a);
+  return cudaGetLastError();
 }
 
 template <typename T>
 static cudaError_t rec3(int d, const Rec3Args& a, cudaStream_t st) {
-  const RecArgs& f = a.fwd;
-  const unsigned n = (unsigned)(f.DV / (f.DV == 16 ? 16 : 32)) * f.H * f.n_seqs;
   switch (d) {
-    case 16: la_rec3_kernel<16, 16, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
-    case 32: la_rec3_kernel<32, 32, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
-    case 64: la_rec3_kernel<64, 32, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
-    case 128: la_rec3_kernel<128, 32, T><<<3 * n, kRecThreads, 0, st>>>(a); break;
-    default: return cudaErrorInvalidValue;
+    case 16: return rec3_launch<16, 16, T>(a, st);
+    case 32: return rec3_launch<32, 32, T>(a, st);
+    case 64: return rec3_launch<64, 32, T>(a, st);
+    case 128: return rec3_launch<128, 32, T>(a, st);
   }
+  return cudaErrorInvalidValue;
+}
+
+template <int DK, int COLS, typename Tin, typename Tout, bool REV>
+static cudaError_t rec_run(const RecArgs& a, cudaStream_t st) {
+  const unsigned n = (unsigned)(a.DV / COLS) * a.H * a.n_seqs;
+  if (a.seg_n > 1) {
+    la_rec_kernel<DK, COLS, Tin, Tout, REV, true><<<n * (a.seg_n - 1), kRecThreads, 0, st>>>(a);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  la_rec_kernel<DK, COLS, Tin, Tout, REV, false><<<n * a.seg_n, kRecThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
 template <int DK, int COLS, typename Tin, typename Tout>
 static cudaError_t rec_launch(const RecArgs& a, bool rev, cudaStream_t st) {
-  const unsigned grid = (unsigned)(a.DV / COLS) * a.H * a.n_seqs;
-  if (rev)
-    la_rec_kernel<DK, COLS, Tin, Tout, true><<<grid, kRecThreads, 0, st>>>(a);
-  else
-    la_rec_kernel<DK, COLS, Tin, Tout, false><<<grid, kRecThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return rev ? rec_run<DK, COLS, Tin, Tout, true>(a, st)
+             : rec_run<DK, COLS, Tin, Tout, false>(a, st);
 }
 
 template <int DK, typename Tin, typename Tout>
@@ -508,12 +617,19 @@ __global__ void __launch_bounds__(kSumThreads) la_dalpha_sum_kernel(const float*
 
 }  // namespace la
 
+size_t la_fwd_simt_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen) {
+  return 4 * la::part_floats(dk, dv, n_seqs, H, la::rec_segments(1, n_seqs, T, H, dv, varlen));
+}
+
 cudaError_t launch_la_fwd_simt(int dtype, int out_dtype, int dk, int dv, const void* q,
                                const void* k, const void* v, const float* alpha, int per_head,
                                const float* S0, const int32_t* cu, void* out, float* S_final,
-                               int n_seqs, int T, int H, int* status, cudaStream_t stream) {
-  const la::RecArgs a{q,   k,       v,  {alpha, H, per_head}, S0, S_final, dv, 1,
-                      out, nullptr, cu, n_seqs, T, H, dv, status};
+                               void* ws, int n_seqs, int T, int H, int* status,
+                               cudaStream_t stream) {
+  la::RecArgs a{q,   k,       v,  {alpha, H, per_head}, S0, S_final, dv, 1,
+                out, nullptr, cu, n_seqs, T, H, dv, status};
+  la::set_parts(&a, dk, la::rec_segments(1, n_seqs, T, H, dv, cu != nullptr),
+                static_cast<float*>(ws));
   return la::rec(dtype, out_dtype, dk, a, false, stream);
 }
 
@@ -523,12 +639,30 @@ cudaError_t launch_la_dalpha_sum(const float* part, float* da, int64_t tokens, i
   return cudaGetLastError();
 }
 
-// S^T and G at the chunks' bounds, then (decay per head) its gradient per token.
+namespace la {
+
+// Segments of the three recurrences (dq, dv, dk), which run together, each
+// with states of its own, when d_k = d_v, and one after another otherwise.
+static void bwd_segments(int dk, int dv, int n_seqs, int T, int H, bool varlen, int* g) {
+  const int together = dk == dv ? 3 : 1;
+  g[0] = g[2] = rec_segments(together, n_seqs, T, H, dk, varlen);
+  g[1] = rec_segments(together, n_seqs, T, H, dv, varlen);
+}
+
+}  // namespace la
+
+// S^T and G at the chunks' bounds, then (decay per head) its gradient per
+// token, then the segments' states.
 size_t la_bwd_simt_workspace_bytes(int dk, int dv, int n_seqs, int T, int H, bool varlen,
                                    bool per_head) {
   const size_t slots = (size_t)la::chunk_slots(varlen, n_seqs, T, la::kChunk);
   const size_t tokens = varlen ? (size_t)T : (size_t)n_seqs * T;
-  return 2 * slots * H * dk * dv * 4 + (per_head ? (tokens * H * 4 + 255) / 256 * 256 : 0);
+  int g[3];
+  la::bwd_segments(dk, dv, n_seqs, T, H, varlen, g);
+  const size_t a = la::part_floats(dk, dv, n_seqs, H, g[0]);
+  const size_t b = la::part_floats(dk, dv, n_seqs, H, g[1]);
+  return 2 * slots * H * dk * dv * 4 + (per_head ? (tokens * H * 4 + 255) / 256 * 256 : 0) +
+         4 * (dk == dv ? 3 * a : (a > b ? a : b));
 }
 
 cudaError_t launch_la_bwd_simt(int dtype, int dk_, int dv_, const void* q, const void* k,
@@ -544,10 +678,16 @@ cudaError_t launch_la_bwd_simt(int dtype, int dk_, int dv_, const void* q, const
   float* part = per_head ? G + slots * H * dk_ * dv_ : dalpha;
   const la::Decay al{alpha, H, per_head};
   // (state, stride of its first index, stride of its second): S^T, G, G^T
-  const la::RecArgs aq{dO, v, k, al, S0, nullptr, 1, dv_, dq, St, cu, n_seqs, T, H, dk_, status};
-  const la::RecArgs av{k, q, dO, al, dSf, dS0, dv_, 1, dv, G, cu, n_seqs, T, H, dv_, status};
-  const la::RecArgs ak{v, dO, q, al, dSf, nullptr, 1, dv_, dk, nullptr, cu, n_seqs, T, H, dk_,
-                       status};
+  la::RecArgs aq{dO, v, k, al, S0, nullptr, 1, dv_, dq, St, cu, n_seqs, T, H, dk_, status};
+  la::RecArgs av{k, q, dO, al, dSf, dS0, dv_, 1, dv, G, cu, n_seqs, T, H, dv_, status};
+  la::RecArgs ak{v, dO, q, al, dSf, nullptr, 1, dv_, dk, nullptr, cu, n_seqs, T, H, dk_, status};
+  int g[3];
+  la::bwd_segments(dk_, dv_, n_seqs, T, H, varlen, g);
+  float* ps = G + slots * H * dk_ * dv_ + (per_head ? ((size_t)tokens * H + 63) / 64 * 64 : 0);
+  const size_t one = dk_ == dv_ ? la::part_floats(dk_, dv_, n_seqs, H, g[0]) : 0;
+  la::set_parts(&aq, dv_, g[0], ps);
+  la::set_parts(&av, dk_, g[1], ps + one);
+  la::set_parts(&ak, dv_, g[2], ps + 2 * one);
   cudaError_t e;
   if (dk_ == dv_) {
     const la::Rec3Args a{aq, {av, ak}};

@@ -177,6 +177,25 @@ def test_few_heads_and_long_sequences(ck, dtype):
             assert torch.equal(o, o2) and torch.equal(S, Sio)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(16, 16), (32, 128), (128, 16), (64, 64), (128, 128)])
+def test_few_heads_forward_and_backward(ck, dk, dv, dtype):
+    """Lengths that a call on the CUDA cores splits into segments, in both directions of time."""
+    for lead, lens, decay in (((1, 700), None, "signed"), ((2, 257), None, "zeros"),
+                              ((900,), [3, 0, 830, 67], "head"), ((1, 1025), None, "one")):
+        cu, n = None, lead[0]
+        if lens:
+            cu, n = torch.tensor([0] + lens, device=DEV).cumsum(0).to(torch.int32), len(lens)
+        q, k, v, a, dO, S0, dSf = make(lead, 1, dk, dv, dtype, decay, seed=dk + dv, n=n)
+        check_fwd(ck, q, k, v, a, S0, cu)
+        check_bwd(ck, q, k, v, a, dO, S0, dSf, cu)
+        check_bwd(ck, q, k, v, a, dO, None, None, cu)
+        Sio = S0.clone()
+        _, S = ck.la_fwd_chunked(q, k, v, a, S0=S0, cu_seqlens=cu)
+        ck.la_fwd_chunked(q, k, v, a, S0=Sio, S_final=Sio, cu_seqlens=cu)
+        assert torch.equal(S, Sio)
+
+
 def test_training_sizes_on_sampled_heads(ck):
     B, T, H = 4, 4096, 16
     q, k, v, a, dO, _, _ = make((B, T), H, 128, 128, torch.bfloat16, seed=8, states=False)
