@@ -661,9 +661,15 @@ static int fwd_segments(int n_seqs, int T, int H, int dv, bool varlen) {
 }
 
 // The first launch leaves the last segment out: smaller pieces fill the SMs.
+// A segment adds up the states of all pieces before it, about 0.7 us each, so
+// that there are no more than eight of them unless the segments alone are more
+// (one head, T = 16384, 16 segments: 98 us with 8 pieces each, 43 with one).
 static int fwd_pieces(int n_seqs, int H, int dv, int segs) {
+  if (segs == 1) return 1;
   const int64_t ctas = (int64_t)n_seqs * H * (dv / fw::BV) * (segs - 1);
-  return segs == 1 ? 1 : (int)(148 / ctas > 8 ? 8 : 148 / ctas < 1 ? 1 : 148 / ctas);
+  const int64_t fill = 148 / ctas, most = 8 / (segs - 1);
+  const int64_t n = fill < most ? fill : most;
+  return n < 1 ? 1 : (int)n;
 }
 
 }  // namespace la

@@ -301,12 +301,16 @@ __global__ void __launch_bounds__(kRecThreads, 4) la_rec3_kernel(const Rec3Args 
 constexpr int rec_columns(int dv) { return dv == 16 ? 16 : 32; }
 
 // Segments per sequence of recurrences with `dv` columns that run together:
-// as many as give every SM four CTAs, if each keeps two chunks.
+// as many as give every SM four CTAs, if each keeps a chunk.  The last segment
+// adds up the states of all others, about 0.8 us each, and a token takes about
+// 0.16 us in the two launches: more than sqrt(T / 5) segments cost more than
+// they give.
 static int rec_segments(int together, int n_seqs, int T, int H, int dv, bool varlen) {
   const int64_t ctas = (int64_t)together * n_seqs * H * (dv / rec_columns(dv));
+  const int64_t len = (int64_t)T / (n_seqs > 0 && varlen ? n_seqs : 1);
   int64_t g = 148 * 4 / (ctas > 0 ? ctas : 1);
-  const int64_t most = (int64_t)T / (n_seqs > 0 && varlen ? n_seqs : 1) / (2 * kChunk);
-  if (g > most) g = most;
+  if (g > len / kChunk) g = len / kChunk;
+  while (g > 1 && 5 * g * g > len) --g;
   return g < 2 ? 1 : (int)g;
 }
 
@@ -415,12 +419,27 @@ struct DalphaArgs {
 constexpr int kDaThreads = 256;
 constexpr int kSlab = 16;  // inner dimension per shared-memory slab (head sizes are multiples)
 
+// Two C x C products at a time (q k^T with do v^T, then q S with k G, whose
+// slabs of S and G also give <S, G>): the next slab's four tiles are on their
+// way in registers while this one's are multiplied.  With few chunks the
+// kernel's time is this chain of slabs; one product at a time without the
+// loads ahead took 105 us per CTA at d_k = 64, d_v = 128.
 template <typename Tin>
-__global__ void __launch_bounds__(kDaThreads) la_dalpha_kernel(const DalphaArgs p) {
-  constexpr int C = kChunk;
+__global__ void __launch_bounds__(kDaThreads, 2) la_dalpha_kernel(const DalphaArgs p) {
+  constexpr int C = kChunk, PT = C * kSlab / kDaThreads;
   __shared__ float sa[C], sx[C], sy[C], head[C], tail[C], zs[kDaThreads / 32];
-  __shared__ float A[kSlab][C + 4], B[kSlab][C + 4];
-  __shared__ float W[C][C + 1], E[C][C + 1];
+  // the tiles, and E in their place once the products are done
+  struct Tiles {
+    float t[4][kSlab][C + 4];
+  };
+  union Scratch {
+    Tiles tiles;
+    float e[C][C + 1];
+  };
+  __shared__ __align__(16) Scratch sc;
+  __shared__ float W[C][C + 1];
+  auto& tl = sc.tiles.t;
+  auto& E = sc.e;
   const int tid = threadIdx.x;
   const int h = blockIdx.y;
   int n, c;
@@ -440,22 +459,29 @@ __global__ void __launch_bounds__(kDaThreads) la_dalpha_kernel(const DalphaArgs 
     sx[tid] = 0.f;
     sy[tid] = 0.f;
   }
-  // acc[a][b] += sum_d Arow[ty * 4 + a][d] * Brow[tx * 4 + b][d]
-  auto rows = [&](const Tin* x, int D, int d0, float (*dst)[C + 4]) {
-    for (int e = tid; e < C * kSlab; e += kDaThreads) {
-      const int r = e / kSlab, d = e % kSlab;
-      dst[d][r] = r < L ? Elem<Tin>::to_f32(x[((size_t)(t0 + r) * p.H + h) * D + d0 + d]) : 0.f;
+  float r[4][PT];  // the next slab's tiles
+  // columns d0 .. d0 + kSlab of a tensor's rows (zero behind the chunk and the head)
+  auto get_rows = [&](float* o, const Tin* x, int D, int d0) {
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+      const int at = tid + e * kDaThreads, row = at / kSlab, d = d0 + at % kSlab;
+      o[e] = row < L && d < D ? Elem<Tin>::to_f32(x[((size_t)(t0 + row) * p.H + h) * D + d]) : 0.f;
     }
   };
-  auto mac = [&](float (*acc)[4]) {
+  auto put_rows = [&](int tile, const float* x) {
+#pragma unroll
+    for (int e = 0; e < PT; ++e) {
+      const int at = tid + e * kDaThreads;
+      tl[tile][at % kSlab][at / kSlab] = x[e];
+    }
+  };
+  // acc[a][b] += sum_d A[d][ty * 4 + a] * B[d][tx * 4 + b]
+  auto mac = [&](float (*acc)[4], int A, int B) {
 #pragma unroll
     for (int d = 0; d < kSlab; ++d) {
-      float a[4], b[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        a[e] = A[d][ty * 4 + e];
-        b[e] = B[d][tx * 4 + e];
-      }
+      const float4 a4 = *reinterpret_cast<const float4*>(&tl[A][d][ty * 4]);
+      const float4 b4 = *reinterpret_cast<const float4*>(&tl[B][d][tx * 4]);
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -463,70 +489,101 @@ __global__ void __launch_bounds__(kDaThreads) la_dalpha_kernel(const DalphaArgs 
     }
   };
   float s1[4][4] = {}, s2[4][4] = {};
-  for (int d0 = 0; d0 < p.DK; d0 += kSlab) {
-    __syncthreads();
-    rows(q, p.DK, d0, A);
-    rows(k, p.DK, d0, B);
-    __syncthreads();
-    mac(s1);
-  }
-  for (int d0 = 0; d0 < p.DV; d0 += kSlab) {
-    __syncthreads();
-    rows(dO, p.DV, d0, A);
-    rows(v, p.DV, d0, B);
-    __syncthreads();
-    mac(s2);
+  {
+    const int D = max(p.DK, p.DV);
+    auto fetch = [&](int d0) {
+      get_rows(r[0], q, p.DK, d0);
+      get_rows(r[1], k, p.DK, d0);
+      get_rows(r[2], dO, p.DV, d0);
+      get_rows(r[3], v, p.DV, d0);
+    };
+    fetch(0);
+    for (int d0 = 0; d0 < D; d0 += kSlab) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 4; ++e) put_rows(e, r[e]);
+      __syncthreads();
+      if (d0 + kSlab < D) fetch(d0 + kSlab);
+      if (d0 < p.DK) mac(s1, 0, 1);
+      if (d0 < p.DV) mac(s2, 2, 3);
+    }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) W[ty * 4 + i][tx * 4 + j] = s1[i][j] * s2[i][j];
 
-  // x and y: rows of [q S] . do and [k G] . v, C columns of the product at a time
+  // x and y: rows of [q S] . do and [k G] . v, C columns of the products at a time
   const size_t st = ((size_t)blockIdx.x * p.H + h) * p.DK * p.DV;
-  for (int which = 0; which < 2; ++which) {
-    const float* M = (which ? p.G : p.St) + st;
+  const float* St = p.St + st;
+  const float* G = p.G + st;
+  float z = 0.f;
+  {
+    // S^T rows run over d_k, G rows over d_v: read along the rows
+    auto fetch = [&](int j0, int d0) {
+      get_rows(r[0], q, p.DK, d0);
+      get_rows(r[1], k, p.DK, d0);
+#pragma unroll
+      for (int e = 0; e < PT; ++e) {
+        const int at = tid + e * kDaThreads;
+        const int js = j0 + at / kSlab, ds = d0 + at % kSlab;
+        const int jg = j0 + at % C, dg = d0 + at / C;
+        r[2][e] = js < p.DV ? St[(size_t)js * p.DK + ds] : 0.f;
+        r[3][e] = jg < p.DV ? G[(size_t)dg * p.DV + jg] : 0.f;
+      }
+    };
+    fetch(0, 0);
     for (int j0 = 0; j0 < p.DV; j0 += C) {
-      float s[4][4] = {};
+      float s[4][4] = {}, g[4][4] = {};
       for (int d0 = 0; d0 < p.DK; d0 += kSlab) {
         __syncthreads();
-        rows(which ? k : q, p.DK, d0, A);
-        for (int e = tid; e < C * kSlab; e += kDaThreads) {
-          // S^T rows run over d_k, G rows over d_v: read along the rows
-          const int j = which ? e % C : e / kSlab, d = which ? e / C : e % kSlab;
-          float x = 0.f;
-          if (j0 + j < p.DV)
-            x = which ? M[(size_t)(d0 + d) * p.DV + j0 + j] : M[(size_t)(j0 + j) * p.DK + d0 + d];
-          B[d][j] = x;
+        put_rows(0, r[0]);
+        put_rows(1, r[1]);
+        put_rows(2, r[2]);
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          const int at = tid + e * kDaThreads;
+          tl[3][at / C][at % C] = r[3][e];
         }
         __syncthreads();
-        mac(s);
+        if (d0 + kSlab < p.DK)
+          fetch(j0, d0 + kSlab);
+        else if (j0 + C < p.DV)
+          fetch(j0 + C, 0);
+        mac(s, 0, 2);
+        mac(g, 1, 3);
+#pragma unroll
+        for (int e = 0; e < PT; ++e) {
+          const int at = tid + e * kDaThreads;
+          z = fmaf(tl[2][at / C][at % C], tl[3][at / C][at % C], z);
+        }
       }
-      const Tin* y = which ? v : dO;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = ty * 4 + i;
-        float part = 0.f;
-        if (r < L) {
+        const int row = ty * 4 + i;
+        float x = 0.f, y = 0.f;
+        if (row < L) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int jj = j0 + tx * 4 + j;
-            if (jj < p.DV)
-              part = fmaf(s[i][j], Elem<Tin>::to_f32(y[((size_t)(t0 + r) * p.H + h) * p.DV + jj]),
-                          part);
+            if (jj < p.DV) {
+              const size_t at = ((size_t)(t0 + row) * p.H + h) * p.DV + jj;
+              x = fmaf(s[i][j], Elem<Tin>::to_f32(dO[at]), x);
+              y = fmaf(g[i][j], Elem<Tin>::to_f32(v[at]), y);
+            }
           }
         }
 #pragma unroll
-        for (int o = 8; o >= 1; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
-        if (tx == 0) (which ? sy : sx)[r] += part;  // one writer per row
+        for (int o = 8; o >= 1; o >>= 1) {
+          x += __shfl_xor_sync(0xffffffffu, x, o);
+          y += __shfl_xor_sync(0xffffffffu, y, o);
+        }
+        if (tx == 0) {  // one writer per row
+          sx[row] += x;
+          sy[row] += y;
+        }
       }
     }
-  }
-  // <S, G>: both read along d_k of S^T
-  float z = 0.f;
-  for (int e = tid; e < p.DK * p.DV; e += kDaThreads) {
-    const int i = e % p.DK, j = e / p.DK;
-    z = fmaf(p.St[st + e], p.G[st + (size_t)i * p.DV + j], z);
   }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
