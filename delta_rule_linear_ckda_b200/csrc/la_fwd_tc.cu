@@ -663,7 +663,7 @@ static int fwd_segments(int n_seqs, int T, int H, int dv, bool varlen) {
 // The first launch leaves the last segment out: smaller pieces fill the SMs.
 // A segment adds up the states of all pieces before it, about 0.7 us each, so
 // that there are no more than eight of them unless the segments alone are more
-// (one head, T = 16384, 16 segments: 98 us with 8 pieces each, 43 with one).
+// (one head, T = 16384, 16 segments: 98 us with 8 pieces each, 57 with one).
 static int fwd_pieces(int n_seqs, int H, int dv, int segs) {
   if (segs == 1) return 1;
   const int64_t ctas = (int64_t)n_seqs * H * (dv / fw::BV) * (segs - 1);

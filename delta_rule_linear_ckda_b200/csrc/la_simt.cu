@@ -14,9 +14,10 @@
 // A recurrence costs 3 d_k d_v fp32 operations per token (the decay and the
 // outer product, the product with the queries): as many as the chunked form
 // with 64-token chunks needs without tensor cores, and it keeps full fp32
-// accuracy.  The kernel is bound by instruction issue.  A CTA owns 32 (16)
-// columns of one (sequence, head)'s state in registers; 4 (8) row groups of
-// 128 threads split the rows.  Two rows share one packed fp32 instruction.
+// accuracy.  The kernel is bound by instruction issue and, with few CTAs, by the
+// latency of a token's chain.  A CTA owns 32 (16) columns of one (sequence,
+// head)'s state in registers; row groups of 128 threads, of one or two columns
+// each, split the rows.  Two rows share one packed fp32 instruction.
 // Tokens come 16 at a time through shared memory, the next 16 already on
 // their way in registers; the row groups' shares of the outputs are summed
 // once per 16 tokens, so no barrier stands between tokens.
@@ -25,7 +26,8 @@
 // tokens take one after another.  Its sequences are then split into segments
 // of whole chunks that run at the same time: a first launch carries each
 // segment's own state to its end (keys and values only), the second starts
-// every segment from their decayed sum.
+// every segment from their decayed sum (backward of B = 2, T = 1000, H = 4,
+// d = 64, fp32, with the decays' gradient: 174 -> 85 us).
 #include "la_common.cuh"
 
 namespace ckda {
@@ -59,17 +61,25 @@ struct RecArgs {
   float* dec;
 };
 
+// Columns per thread: what a thread reads of k and q from shared memory serves
+// all of its columns.  Two, if that leaves a thread four rows (the backward's
+// second launch, d = 128, B = 4, T = 2048, H = 4: 339 us with one column, 318
+// with two).
+template <int DK, int COLS>
+constexpr int kCpt = DK * COLS / kRecThreads >= 8 ? 2 : 1;
+
 template <int DK, int COLS>
 struct RecSmem {
   float sq[kTile][DK], sk[kTile][DK], sv[kTile][COLS], sa[kTile];
-  float red[kTile][kRecThreads / COLS][COLS];
+  float red[kTile][kRecThreads * kCpt<DK, COLS> / COLS][COLS];
 };
 
 // SUM: the segments' own end states only (all but the last segment)
 template <int DK, int COLS, typename Tin, typename Tout, bool REV, bool SUM>
 __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSmem<DK, COLS>& sm) {
-  constexpr int RG = kRecThreads / COLS;  // row groups
-  constexpr int RPT = DK / RG;            // rows per thread
+  constexpr int CPT = kCpt<DK, COLS>;           // columns per thread
+  constexpr int RG = kRecThreads * CPT / COLS;  // row groups
+  constexpr int RPT = DK / RG;                  // rows per thread
   constexpr int LQ = kTile * DK / kRecThreads;
   constexpr int LV = kTile * COLS / kRecThreads;
   static_assert(RPT % 2 == 0 && LQ >= 1 && LV >= 1, "shape");
@@ -80,7 +90,7 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
   auto& red = sm.red;
 
   const int tid = threadIdx.x;
-  const int col = tid % COLS, g = tid / COLS;
+  const int col = tid % (COLS / CPT) * CPT, g = tid / (COLS / CPT);
   // block index: column slice, then segment, then head, then sequence (longest first)
   const int slices = p.DV / COLS, nseg = SUM ? p.seg_n - 1 : p.seg_n;
   const int j0 = (int)(block % slices) * COLS;
@@ -108,27 +118,33 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
 
   const size_t unit = (size_t)n * p.H + h, st0 = unit * DK * p.DV;
   const int i0 = g * RPT;
-  // this thread's column of part's states
+  // this thread's columns of part's states
   float* part = p.part + unit * p.seg_n * DK * p.DV + (size_t)i0 * p.DV + j0 + col;
-  auto put_part = [&](int at, const float2* x) {
-    float* o = part + (size_t)at * DK * p.DV;
-#pragma unroll
-    for (int r = 0; r < RPT / 2; ++r) {
-      o[(size_t)(2 * r) * p.DV] = x[r].x;
-      o[(size_t)(2 * r + 1) * p.DV] = x[r].y;
-    }
-  };
-  float2 X[RPT / 2];
-#pragma unroll
-  for (int r = 0; r < RPT / 2; ++r) X[r] = make_float2(0.f, 0.f);
-  if (p.X0 != nullptr && (SUM ? seg == 0 : p.seg_n == 1)) {
-    const float* b = p.X0 + st0 + (size_t)(j0 + col) * p.sj;
+  float2 X[CPT][RPT / 2];
+  auto put = [&](float* o) {  // rows of p.DV columns
 #pragma unroll
     for (int r = 0; r < RPT / 2; ++r)
-      X[r] = make_float2(b[(size_t)(i0 + 2 * r) * p.si], b[(size_t)(i0 + 2 * r + 1) * p.si]);
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) {
+        o[(size_t)(2 * r) * p.DV + c] = X[c][r].x;
+        o[(size_t)(2 * r + 1) * p.DV + c] = X[c][r].y;
+      }
+  };
+#pragma unroll
+  for (int c = 0; c < CPT; ++c)
+#pragma unroll
+    for (int r = 0; r < RPT / 2; ++r) X[c][r] = make_float2(0.f, 0.f);
+  if (p.X0 != nullptr && (SUM ? seg == 0 : p.seg_n == 1)) {
+#pragma unroll
+    for (int c = 0; c < CPT; ++c) {
+      const float* b = p.X0 + st0 + (size_t)(j0 + col + c) * p.sj;
+#pragma unroll
+      for (int r = 0; r < RPT / 2; ++r)
+        X[c][r] = make_float2(b[(size_t)(i0 + 2 * r) * p.si], b[(size_t)(i0 + 2 * r + 1) * p.si]);
+    }
     // (the second launch starts from a copy: its last segment may write Xf
     // over X0 before its first one starts)
-    if constexpr (SUM) put_part(0, X);
+    if constexpr (SUM) put(part);
   }
   if (!SUM && p.seg_n > 1) {
     float f = 1.f;
@@ -138,9 +154,11 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
         const float* b = part + (size_t)e * DK * p.DV;
         const float2 f2 = make_float2(f, f);
 #pragma unroll
-        for (int r = 0; r < RPT / 2; ++r)
-          X[r] = fma2(f2, make_float2(b[(size_t)(2 * r) * p.DV], b[(size_t)(2 * r + 1) * p.DV]),
-                      X[r]);
+        for (int c = 0; c < CPT; ++c)
+#pragma unroll
+          for (int r = 0; r < RPT / 2; ++r)
+            X[c][r] = fma2(f2, make_float2(b[(size_t)(2 * r) * p.DV + c],
+                                           b[(size_t)(2 * r + 1) * p.DV + c]), X[c][r]);
       }
       if (e > 0) f *= p.dec[unit * p.seg_n + e - 1];
     }
@@ -195,33 +213,39 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
     if (it + 1 < mine) fetch(REV ? tl - 1 : tl + 1);
 
     if (!SUM && p.kept != nullptr && (REV ? (tl % per == per - 1 || tl == ntiles - 1) : tl % per == 0)) {
-      float* o = p.kept + ((size_t)(slot0 + tl / per) * p.H + h) * DK * p.DV + j0 + col;
-#pragma unroll
-      for (int r = 0; r < RPT / 2; ++r) {
-        o[(size_t)(i0 + 2 * r) * p.DV] = X[r].x;
-        o[(size_t)(i0 + 2 * r + 1) * p.DV] = X[r].y;
-      }
+      put(p.kept + ((size_t)(slot0 + tl / per) * p.H + h) * DK * p.DV + (size_t)i0 * p.DV + j0 + col);
     }
     // Backward in time the decay of token t acts behind its own term: it is
     // applied with token t - 1's, and the tile's first token's at the end.
     // Four tokens at a time, so that one's loads from shared memory and sums
     // run under another's.
     auto token = [&](int t, float a) {
-      const float vv = sv[t][col];
-      const float2 a2 = make_float2(a, a), v2 = make_float2(vv, vv);
-      float2 o = make_float2(0.f, 0.f), o1 = o;
+      const float2 a2 = make_float2(a, a);
+      float2 o[CPT], o1[CPT];
+#pragma unroll
+      for (int c = 0; c < CPT; ++c) o[c] = o1[c] = make_float2(0.f, 0.f);
 #pragma unroll
       for (int r = 0; r < RPT / 2; ++r) {
         const float2 k2 = *reinterpret_cast<const float2*>(&sk[t][i0 + 2 * r]);
-        X[r] = fma2(X[r], a2, mul2(k2, v2));
-        if constexpr (SUM) continue;
-        const float2 q2 = *reinterpret_cast<const float2*>(&sq[t][i0 + 2 * r]);
-        if (r & 1)
-          o1 = fma2(q2, X[r], o1);
-        else
-          o = fma2(q2, X[r], o);
+        float2 q2 = k2;
+        if constexpr (!SUM) q2 = *reinterpret_cast<const float2*>(&sq[t][i0 + 2 * r]);
+#pragma unroll
+        for (int c = 0; c < CPT; ++c) {
+          const float vv = sv[t][col + c];
+          X[c][r] = fma2(X[c][r], a2, mul2(k2, make_float2(vv, vv)));
+          if constexpr (!SUM) {
+            if (r & 1)
+              o1[c] = fma2(q2, X[c][r], o1[c]);
+            else
+              o[c] = fma2(q2, X[c][r], o[c]);
+          }
+        }
       }
-      if constexpr (!SUM) red[t][g][col] = (o.x + o1.x) + (o.y + o1.y);
+      if constexpr (!SUM) {
+#pragma unroll
+        for (int c = 0; c < CPT; ++c)
+          red[t][g][col + c] = (o[c].x + o1[c].x) + (o[c].y + o1[c].y);
+      }
     };
     if (rows == kTile) {
 #pragma unroll 4
@@ -239,7 +263,9 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
     if (REV) {
       const float2 a2 = make_float2(sa[0], sa[0]);
 #pragma unroll
-      for (int r = 0; r < RPT / 2; ++r) X[r] = mul2(X[r], a2);
+      for (int c = 0; c < CPT; ++c)
+#pragma unroll
+        for (int r = 0; r < RPT / 2; ++r) X[c][r] = mul2(X[c][r], a2);
     }
     if constexpr (SUM) continue;
     __syncthreads();
@@ -258,7 +284,7 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
     }
   }
   if constexpr (SUM) {
-    put_part(seg + 1, X);
+    put(part + (size_t)(seg + 1) * DK * p.DV);
     if (tid < kTile) {
 #pragma unroll
       for (int o = kTile / 2; o >= 1; o >>= 1)
@@ -266,11 +292,14 @@ __device__ __forceinline__ void rec_body(const RecArgs& p, unsigned block, RecSm
       if (tid == 0 && j0 == 0) p.dec[unit * p.seg_n + seg] = (float)total;
     }
   } else if (p.Xf != nullptr && seg == p.seg_n - 1) {
-    float* b = p.Xf + st0 + (size_t)(j0 + col) * p.sj;
 #pragma unroll
-    for (int r = 0; r < RPT / 2; ++r) {
-      b[(size_t)(i0 + 2 * r) * p.si] = X[r].x;
-      b[(size_t)(i0 + 2 * r + 1) * p.si] = X[r].y;
+    for (int c = 0; c < CPT; ++c) {
+      float* b = p.Xf + st0 + (size_t)(j0 + col + c) * p.sj;
+#pragma unroll
+      for (int r = 0; r < RPT / 2; ++r) {
+        b[(size_t)(i0 + 2 * r) * p.si] = X[c][r].x;
+        b[(size_t)(i0 + 2 * r + 1) * p.si] = X[c][r].y;
+      }
     }
   }
 }
@@ -475,20 +504,33 @@ __global__ void __launch_bounds__(kDaThreads, 2) la_dalpha_kernel(const DalphaAr
       tl[tile][at % kSlab][at / kSlab] = x[e];
     }
   };
-  // acc[a][b] += sum_d A[d][ty * 4 + a] * B[d][tx * 4 + b]
-  auto mac = [&](float (*acc)[4], int A, int B) {
+  // acc[a][b] += sum_d A[d][ty * 4 + a] * B[d][tx * 4 + b], two b at a time
+  struct Acc {
+    float2 x[4][2];
+    __device__ __forceinline__ Acc() {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = make_float2(0.f, 0.f);
+    }
+    __device__ __forceinline__ float at(int i, int j) const {
+      return j & 1 ? x[i][j / 2].y : x[i][j / 2].x;
+    }
+  };
+  auto mac = [&](Acc& acc, int A, int B) {
 #pragma unroll
     for (int d = 0; d < kSlab; ++d) {
       const float4 a4 = *reinterpret_cast<const float4*>(&tl[A][d][ty * 4]);
       const float4 b4 = *reinterpret_cast<const float4*>(&tl[B][d][tx * 4]);
-      const float a[4] = {a4.x, a4.y, a4.z, a4.w}, b[4] = {b4.x, b4.y, b4.z, b4.w};
+      const float a[4] = {a4.x, a4.y, a4.z, a4.w};
+      const float2 b0 = make_float2(b4.x, b4.y), b1 = make_float2(b4.z, b4.w);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      for (int i = 0; i < 4; ++i) {
+        const float2 aa = make_float2(a[i], a[i]);
+        acc.x[i][0] = fma2(aa, b0, acc.x[i][0]);
+        acc.x[i][1] = fma2(aa, b1, acc.x[i][1]);
+      }
     }
   };
-  float s1[4][4] = {}, s2[4][4] = {};
+  Acc s1, s2;
   {
     const int D = max(p.DK, p.DV);
     auto fetch = [&](int d0) {
@@ -511,7 +553,7 @@ __global__ void __launch_bounds__(kDaThreads, 2) la_dalpha_kernel(const DalphaAr
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) W[ty * 4 + i][tx * 4 + j] = s1[i][j] * s2[i][j];
+    for (int j = 0; j < 4; ++j) W[ty * 4 + i][tx * 4 + j] = s1.at(i, j) * s2.at(i, j);
 
   // x and y: rows of [q S] . do and [k G] . v, C columns of the products at a time
   const size_t st = ((size_t)blockIdx.x * p.H + h) * p.DK * p.DV;
@@ -534,7 +576,7 @@ __global__ void __launch_bounds__(kDaThreads, 2) la_dalpha_kernel(const DalphaAr
     };
     fetch(0, 0);
     for (int j0 = 0; j0 < p.DV; j0 += C) {
-      float s[4][4] = {}, g[4][4] = {};
+      Acc s, g;
       for (int d0 = 0; d0 < p.DK; d0 += kSlab) {
         __syncthreads();
         put_rows(0, r[0]);
@@ -568,8 +610,8 @@ __global__ void __launch_bounds__(kDaThreads, 2) la_dalpha_kernel(const DalphaAr
             const int jj = j0 + tx * 4 + j;
             if (jj < p.DV) {
               const size_t at = ((size_t)(t0 + row) * p.H + h) * p.DV + jj;
-              x = fmaf(s[i][j], Elem<Tin>::to_f32(dO[at]), x);
-              y = fmaf(g[i][j], Elem<Tin>::to_f32(v[at]), y);
+              x = fmaf(s.at(i, j), Elem<Tin>::to_f32(dO[at]), x);
+              y = fmaf(g.at(i, j), Elem<Tin>::to_f32(v[at]), y);
             }
           }
         }

@@ -555,7 +555,8 @@ enum {
  *                may be q and k themselves when those are contiguous and of
  *                the same type, and overlap nothing otherwise.
  *   d in {16, 32, 64, 128}; rot a multiple of 8, 0 <= rot <= d; eps >= 0 (a
- *   row of zeros with eps = 0 gives zeros).
+ *   row of zeros with eps = 0 gives zeros).  |x|^2 is an fp32 sum: a row for
+ *   which it overflows, or is zero with eps = 0, gives zeros.
  */
 CKDA_API int ckda_qk_norm_rope(const void* q, const void* k, const float* wq, const float* wk,
                                const int32_t* positions, const float* inv_freq, void* q_out,
