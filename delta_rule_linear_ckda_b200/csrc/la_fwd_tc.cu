@@ -35,6 +35,13 @@
 // with the terms side by side (N = 192): shared memory, whose bandwidth bounds
 // this kernel, is read for K once instead of three times.
 //
+// P is zero right of the diagonal, but zero times a v that is not finite is
+// not: such values are taken out of V's tile (never out of the state's
+// operand) and the rows from their token on set to NaN, which is what the
+// state, now NaN in that column, gives the later chunks.  Rows before it keep
+// their values.  The check takes 2 % of the time (prefill 90.8 -> 92.6 us), in
+// the conversion or after it behind a barrier of its own alike.
+//
 // A sequence may be split into segments that run at the same time (few
 // sequences and heads): a first launch computes each segment's own end state
 // (K, V only), the second starts every segment from their decayed sum.
@@ -64,8 +71,11 @@ constexpr uint32_t OFF_SB = OFF_VW + 3 * 16384;  // bf16 state [128][64]
 constexpr uint32_t OFF_DEC = OFF_SB + 16384;     // 2 x the decays (put_decays)
 constexpr uint32_t kDecBytes = kDecFloats * 4;
 constexpr uint32_t OFF_BAR = OFF_DEC + 2 * kDecBytes;
-constexpr uint32_t OFF_MISC = OFF_BAR + 176;     // tensor-memory base, the sequence
-constexpr uint32_t kSmem = OFF_MISC + 16;
+constexpr uint32_t OFF_MISC = OFF_BAR + 176;     // tensor-memory base, the sequence, whether any
+                                                 // column has what follows
+constexpr uint32_t OFF_BAD = OFF_MISC + 16;      // a column's first token (of this block's) whose v
+                                                 // is not finite
+constexpr uint32_t kSmem = OFF_BAD + 4 * BV;
 static_assert(kSmem <= 232448, "shared memory");
 
 // mbarriers, byte offsets from OFF_BAR; each completes once per chunk (those
@@ -75,7 +85,7 @@ constexpr uint32_t B_SC = 48;    // Q K^T complete (tensor core); the last chunk
 constexpr uint32_t B_P = 56;     // P written, the scores read
 constexpr uint32_t B_VW = 64;    // diag(suf) V written, V's and K's tail rows cleared, the last
                                  // chunk's product read
-constexpr uint32_t B_SB = 72;    // the state's operand written
+constexpr uint32_t B_SB = 72;    // the state's operand written, V finite
 constexpr uint32_t B_O = 80;     // Q S and P V complete (tensor core)
 constexpr uint32_t B_OE = 88;    // and read
 // complete (tensor core), + 8 (c & 1): the copy thread, which nothing holds
@@ -172,6 +182,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     tmem_alloc(sb + OFF_MISC, kTmemCols);
     tmem_relinquish();
   }
+  int* bad_any = reinterpret_cast<int*>(sm + OFF_MISC + 8);
+  int* bad_from = reinterpret_cast<int*>(sm + OFF_BAD);
+  if constexpr (!SUM) {
+    if (tid < BV) bad_from[tid] = INT32_MAX;
+    if (tid == 0) *bad_any = 0;
+  }
   if constexpr (KD < DK) {  // no load writes K's second 64 columns
     for (int e = tid; e < 2 * 16384 / 16; e += kThreads)
       *reinterpret_cast<uint4*>(sm + OFF_K + (e >> 10) * 32768 + 16384 + (e & 1023) * 16) =
@@ -244,6 +260,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (!(ok = wait(B_O, e))) break;
           tc_fence_after();
           const bool st = staged(e), in = i < len_of(e);
+          const bool bad = *reinterpret_cast<volatile int*>(bad_any) != 0;
           Tout* o = static_cast<Tout*>(p.out) +
                     ((size_t)(tok0 + (int64_t)e * C + i) * p.H + h) * p.DV + j0 + kHalf * hf;
 #pragma unroll 1
@@ -254,6 +271,12 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             tmem_ld_wait();
 #pragma unroll
             for (int u = 0; u < 16; ++u) x[u] = fmaf(pre, y[u], x[u]);
+            if (__builtin_expect(bad, 0)) {
+#pragma unroll
+              for (int u = 0; u < 16; ++u)
+                if (reinterpret_cast<volatile int*>(bad_from)[kHalf * hf + u0 + u] <= e * C + i)
+                  x[u] = __int_as_float(0x7fffffff);
+            }
             if (st) {
 #pragma unroll
               for (int c8 = 0; c8 < 2; ++c8)
@@ -395,6 +418,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // not wait for the queries' product with the last chunk's state
       const int st = c & 1;
       const int len = len_of(c);
+      uint32_t zero = 0;  // this thread's V times zero: a pair of zeros if all of it is finite
       if (!(ok = wait(B_DEC + 8 * st, c >> 1))) break;
       {
         const float4 tot = *reinterpret_cast<const float4*>(tots(c));
@@ -415,7 +439,11 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint32_t in[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
             uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) split3(in[e], w2, &t1[e], &t2[e], &t3[e]);
+            for (int e = 0; e < 8; ++e) {
+              split3(in[e], w2, &t1[e], &t2[e], &t3[e]);
+              if constexpr (!SUM)
+                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zero) : "r"(in[e]), "r"(0));
+            }
             uint8_t* d = sm + OFF_VW;
             *reinterpret_cast<uint4*>(d + o0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
             *reinterpret_cast<uint4*>(d + o1) = make_uint4(t1[4], t1[5], t1[6], t1[7]);
@@ -446,6 +474,18 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       tc_fence_before();
       arrive(B_VW);
       if constexpr (!SUM) {
+        if (__builtin_expect((zero & 0x7fff7fffu) != 0, 0)) {
+#pragma unroll 1
+          for (int e = kHalf * hf; e < kHalf * (hf + 1); ++e) {
+            uint16_t* x = reinterpret_cast<uint16_t*>(sm + OFF_V + st * 16384 +
+                                                      sw128_chunk(r, e & ~7, 128)) + (e & 7);
+            if ((*x & 0x7f80) == 0x7f80) {
+              *x = 0;
+              atomicMin(bad_from + e, c * C + r);
+            }
+          }
+          *reinterpret_cast<volatile int*>(bad_any) = 1;
+        }
         // (the old operand has been read)
         if (c > 0 && !(ok = wait(B_QS + 8 * (st ^ 1), (c - 1) >> 1))) break;
 #pragma unroll

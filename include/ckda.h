@@ -489,8 +489,9 @@ CKDA_API int ckda_sfda_decode_step(const void* q, const void* k, const void* v,
  * bf16 inputs with d_k, d_v in {64, 128} run on the tensor cores: the scores
  * (times their decays) and the copy of the state that the queries read are
  * rounded to bf16 once each, all sums are fp32, and S_final keeps fp32
- * accuracy.  A value that is not finite in a sequence reaches that sequence's
- * outputs only.
+ * accuracy.  A value that is not finite reaches the outputs that the recurrence
+ * leads it to and no others: tokens before it, other heads and other sequences
+ * keep their values.
  */
 CKDA_API int ckda_la_fwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
                                  const float* S0, const int32_t* cu_seqlens, void* out,
