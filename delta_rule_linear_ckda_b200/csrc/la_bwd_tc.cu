@@ -690,10 +690,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             if (J == w4 || len < C) {
               const int last = in ? (J == w4 ? lane : 31) : -1;
 #pragma unroll
-              for (int t = 0; t < 8; ++t) {
-                s1[t] = e + t <= last ? s1[t] * s2[t] : 0.f;
-                dd[e + t] = e + t <= last ? dd[e + t] : 0.f;
-              }
+              for (int t = 0; t < 8; ++t) s1[t] = e + t <= last ? s1[t] * s2[t] : 0.f;
             } else {
 #pragma unroll
               for (int t = 0; t < 8; ++t) s1[t] *= s2[t];
@@ -710,6 +707,12 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
               dd[e + t + 3] *= R;
               R = fmaf(f.w, R, s1[t + 3]);
             }
+          }
+          if (J == w4 || len < C) {
+            // (after the product with R, which need not be finite by now)
+            const int last = in ? (J == w4 ? lane : 31) : -1;
+#pragma unroll
+            for (int t = 0; t < 32; ++t) dd[t] = t <= last ? dd[t] : 0.f;
           }
           // lane t gets the sum of dd[t] over the lanes
 #pragma unroll

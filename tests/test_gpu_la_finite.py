@@ -80,3 +80,25 @@ def test_many_values_that_are_not_finite(ck):  # noqa: F811
     for b, n in enumerate((1, 130, 333)):
         assert torch.equal(o[b, :n], ref[b, :n]) and not torch.isfinite(o[b, n:]).any()
         assert not torch.isfinite(S[b]).any()
+
+
+def backward_cases(ck, which, dk, dv, dtype):  # noqa: F811
+    """(call, 64-bit gradients, tolerances) with one value of ``which`` not finite."""
+    q, k, v, a, dO, S0, dSf = make((1, 300), 2, dk, dv, dtype, "signed", seed=dk)
+    clean = dict(q=q, k=k, v=v, alpha=a, dO=dO)
+    tol = la_ref.tol_backward(*clean.values(), S0, dSf, tensor_core=tensor_core(ck, dk, dv, dtype))
+    for i, (t, c) in enumerate(PLACES):
+        args = dict(clean)
+        args[which] = spoil(clean[which], t, c, BAD[i % 3])
+        g = ck.la_bwd_chunked(**args, S0=S0, dS_final=dSf)
+        assert ck.device_status() == 0
+        yield t, g, la_ref.backward(*args.values(), S0, dSf), tol
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128), (32, 16)])
+@pytest.mark.parametrize("which", ["q", "k", "v", "alpha", "dO"])
+def test_decays_gradient(ck, which, dk, dv, dtype):  # noqa: F811
+    for t, g, ref, tol in backward_cases(ck, which, dk, dv, dtype):
+        for n in ("dalpha", "dS0"):
+            compare(g[n], ref[n], tol[n], f"{n} {which} {t}")
