@@ -23,6 +23,12 @@
 //     (V G^T: one), because x, y and so the decays' gradient keep fp32
 //     accuracy; dq, dk, dv are rounded to bf16 in the end, and E, P once on
 //     the way.
+// E and P are zero right of the diagonal, but zero times a value that is not
+// finite is not, and E K, E^T Q and P^T dO would carry it to tokens that do
+// not depend on it.  A chunk with such a value shows it in the scores'
+// diagonal; it takes those values out of K, Q and dO before these products (E K
+// then waits for the other readers of K) and sets what does depend on them to
+// NaN afterwards.
 // Bound by HBM bandwidth and by the chunk kernel's chain of phases; the two
 // states of 64 KB per (chunk, head), written and read once, are more than half
 // of the traffic.
@@ -346,14 +352,19 @@ constexpr uint32_t OFF_F = 229376;                   // floats, below
 constexpr uint32_t F_A = 0, F_SW = 128, F_TOT = 256, F_Z = 260, F_X = 268, F_COL = 524;
 // later in their places: y by column half, the sums within the chunk
 constexpr uint32_t F_Y0 = F_COL, F_Y1 = F_SW, F_IN = F_X + 128;
+// bytes, of a chunk with values that are not finite: the row behind a
+// column's last one in Q, in dO (the first one in K: OFF_KBAD)
+constexpr uint32_t OFF_QBAD = OFF_F + 4 * 652, OFF_OBAD = OFF_QBAD + 128;
 constexpr uint32_t OFF_BAR = OFF_F + 4 * 716;
 constexpr uint32_t B_LD = 0;    // tiles loaded
 constexpr uint32_t B_SC = 8;    // scores complete (tensor core)
 constexpr uint32_t B_DS = 16;   // dO S^T complete
 constexpr uint32_t B_G = 24;    // a term of G is done with (three times per unit)
 constexpr uint32_t B_FIN = 32;  // the gradients complete
-constexpr uint32_t OFF_MISC = OFF_BAR + 40;
-constexpr uint32_t kSmem = OFF_MISC + 16;
+constexpr uint32_t OFF_MISC = OFF_BAR + 40;  // tensor-memory base, whether the chunk has such values
+constexpr uint32_t OFF_KBAD = OFF_MISC + 16;
+constexpr uint32_t kSmem = OFF_KBAD + 128;
+static_assert(OFF_OBAD + 128 <= OFF_BAR, "bytes of a chunk with values that are not finite");
 static_assert(kSmem <= 232448, "shared memory");
 
 constexpr uint32_t TM_S1 = 0, TM_S2 = 128;           // Q K^T, dO V^T
@@ -439,6 +450,40 @@ __device__ __forceinline__ float scale_rows(uint32_t addr, float f, const uint8_
   }
   tmem_st_wait();
   return s;
+}
+
+// Takes the values that are not finite out of a column of a 128-row tile; their
+// first row (128 if there is none) and the row behind the last (0).
+__device__ __forceinline__ void clean_column(uint8_t* tile, int col, int* first, int* end) {
+  *first = 128;
+  *end = 0;
+#pragma unroll 1
+  for (int r = 0; r < 128; ++r) {
+    uint16_t* x = reinterpret_cast<uint16_t*>(tile + sw128_chunk(r, col & ~7, 128)) + (col & 7);
+    if ((*x & 0x7f80) == 0x7f80) {
+      *x = 0;
+      if (*end == 0) *first = r;
+      *end = r + 1;
+    }
+  }
+}
+
+// Sets row i of N columns of an accumulator to NaN where it lies in rows
+// [at[col], 128) or, for `before`, in rows [0, at[col]).
+template <int N>
+__device__ __forceinline__ void poison_rows(uint32_t addr, int i, const uint8_t* at, bool before) {
+#pragma unroll 1
+  for (int e = 0; e < N; e += 16) {
+    float x[16];
+    tmem_ld16(addr + e, x);
+    tmem_ld_wait();
+    uint32_t y[16];
+#pragma unroll
+    for (int t = 0; t < 16; ++t)
+      y[t] = (i < at[e + t]) == before ? 0x7fffffffu : __float_as_uint(x[t]);
+    tmem_st16(addr + e, y);
+  }
+  tmem_st_wait();
 }
 
 template <int KD, int DV>  // d_k, d_v
@@ -558,6 +603,8 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             make_uint4(w[0], w[1], w[2], w[3]);
       }
     };
+    volatile int* odd = reinterpret_cast<volatile int*>(sm + OFF_MISC + 4);
+    if (tid == 0) *odd = 0;  // (the last unit's was read before its last barriers)
     float z = 0.f;
 #pragma unroll
     for (int e = 0; e < DV / 2; ++e) z = fmaf(S[e], G[e], z);
@@ -732,6 +779,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             F[F_COL + 32 * (w4 * (w4 - 1) / 2 + J) + lane] = cs;
         }
       } else {
+        float2 zero = make_float2(0.f, 0.f);  // NaN, if the diagonal block is not finite
 #pragma unroll 1
         for (int J = 0; J < 4; ++J) {
           const float d = J < w4 ? pw * between(J) : 0.f;
@@ -769,6 +817,11 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
 #pragma unroll
               for (int t = 0; t < 16; ++t) s1[t] = s2[t] = 0.f;
             }
+            if (J == w4) {
+#pragma unroll
+              for (int t = 0; t < 16; ++t)
+                zero = fma2(make_float2(s1[t], s2[t]), make_float2(0.f, 0.f), zero);
+            }
 #pragma unroll
             for (int t = 0; t < 16; t += 8) {
               const uint32_t o = sw128_chunk(i, 32 * J + e + t, 128);
@@ -777,6 +830,7 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
             }
           }
         }
+        if (!(zero.x + zero.y == 0.f)) *odd = 1;
         fence_proxy_async_smem();
       }
       tc_fence_before();
@@ -784,8 +838,11 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
     ok = __syncthreads_and(ok);
     if (!ok) break;
 
+    const bool rare = *odd != 0;  // (of the whole block)
+
     // ---- K G and V G^T with G's first term; x; diag(pre) dO S^T ---------------------------
     constexpr uint32_t id_kg = idesc_bf16(128, DV, 0, 1), id_vg = idesc_bf16(128, KD, 0, 0);
+    constexpr uint32_t id_ek = idesc_bf16(128, KD, 0, 1);
     if (lead) {
       tc_fence_after();
       if (elect_one()) {
@@ -825,9 +882,10 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
         for (int kk = 0; kk < KD / 16; ++kk)
           mma_f16(tmem + TM_DV, km(1, kk), mn(6, kk), id_kg, 1u);
         mma_commit(bar + B_G);
-        constexpr uint32_t id = idesc_bf16(128, KD, 0, 1);
+        if (!rare) {
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DQ, km(4, kk), mn(1, kk), id, 1u);
+          for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DQ, km(4, kk), mn(1, kk), id_ek, 1u);
+        }
       }
       __syncwarp();
       issued = B_G;
@@ -867,6 +925,24 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       const float y = scale_rows<DV / 2>(row + TM_DV + DV / 2 * hf, suf, sm + OFF_V, i, DV / 2 * hf);
       F[(hf ? F_Y1 : F_Y0) + i] = i < len ? y : 0.f;
       scale_rows<KD / 2>(row + TM_DK + KD / 2 * hf, suf, nullptr, i, 0);
+      if (__builtin_expect(rare && ok, 0)) {
+        // (all readers of K but E K are through, and of Q and dO but E^T Q and P^T dO)
+#pragma unroll 1
+        for (int x = tid; x < 2 * KD + DV; x += kCompute) {
+          int first, end;
+          if (x < KD) {
+            clean_column(sm + OFF_K, x, &first, &end);
+            sm[OFF_KBAD + x] = (uint8_t)first;
+          } else if (x < 2 * KD) {
+            clean_column(sm + OFF_Q, x - KD, &first, &end);
+            sm[OFF_QBAD + x - KD] = (uint8_t)end;
+          } else {
+            clean_column(sm + OFF_DO, x - 2 * KD, &first, &end);
+            sm[OFF_OBAD + x - 2 * KD] = (uint8_t)end;
+          }
+        }
+        fence_proxy_async_smem();
+      }
       tc_fence_before();
     }
     ok = __syncthreads_and(ok);
@@ -877,6 +953,10 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
       tc_fence_after();
       if (elect_one()) {
         constexpr uint32_t id_dv = idesc_bf16(128, DV, 1, 1), id_dk = idesc_bf16(128, KD, 1, 1);
+        if (rare) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DQ, km(4, kk), mn(1, kk), id_ek, 1u);
+        }
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) mma_f16(tmem + TM_DV, mn(5, kk), mn(3, kk), id_dv, 1u);
 #pragma unroll
@@ -939,6 +1019,11 @@ la_chunk_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant_
           loaded = true;
           ld_par = ph ^ 1u;
         }
+      }
+      if (__builtin_expect(rare && ok, 0)) {
+        poison_rows<KD / 2>(row + TM_DQ + KD / 2 * hf, i, sm + OFF_KBAD + KD / 2 * hf, false);
+        poison_rows<KD / 2>(row + TM_DK + KD / 2 * hf, i, sm + OFF_QBAD + KD / 2 * hf, true);
+        poison_rows<DV / 2>(row + TM_DV + DV / 2 * hf, i, sm + OFF_OBAD + DV / 2 * hf, true);
       }
       // the gradients' rows: whole chunks leave by TMA from the tiles of E, P
       // and G's terms, a partial one row by row

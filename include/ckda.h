@@ -510,7 +510,8 @@ CKDA_API int64_t ckda_la_fwd_workspace_bytes(int B, int T, int H, int d_k, int d
  * zero decay is that of the recurrence (no division by a_t).  No output may
  * overlap another tensor.  Every output element is written by every call, sums
  * are in a fixed order: the same call gives the same bits.  dalpha and dS0
- * keep fp32 accuracy with bf16 inputs too.
+ * keep fp32 accuracy with bf16 inputs too.  A value that is not finite reaches
+ * the gradients that depend on it and no others.
  */
 CKDA_API int ckda_la_bwd_chunked(const void* q, const void* k, const void* v, const float* alpha,
                                  const float* S0, const int32_t* cu_seqlens, const void* dO,

@@ -102,3 +102,32 @@ def test_decays_gradient(ck, which, dk, dv, dtype):  # noqa: F811
     for t, g, ref, tol in backward_cases(ck, which, dk, dv, dtype):
         for n in ("dalpha", "dS0"):
             compare(g[n], ref[n], tol[n], f"{n} {which} {t}")
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 64), (128, 64), (64, 128), (32, 16)])
+@pytest.mark.parametrize("which", ["q", "k", "v", "alpha", "dO"])
+def test_backward(ck, which, dk, dv, dtype):  # noqa: F811
+    for t, g, ref, tol in backward_cases(ck, which, dk, dv, dtype):
+        for n in ref:
+            compare(g[n], ref[n], tol[n], f"{n} {which} {t}")
+
+
+def test_backward_after_and_before_other_chunks(ck):  # noqa: F811
+    """More (chunk, head) pairs than SMs: the neighbours of a pair with such a value, in the
+    same block's walk too, keep their results bit for bit."""
+    q, k, v, a, dO, S0, dSf = make((4, 300), 40, 64, 64, torch.bfloat16, "signed", seed=3)
+    g = ck.la_bwd_chunked(q, k, v, a, dO, S0=S0, dS_final=dSf)
+    w = [x.clone() for x in (q, k, v, dO)]
+    hit = torch.zeros(4, 40, dtype=torch.bool, device=DEV)
+    for j in range(16):
+        b, t, h = j % 4, 37 + 16 * j, (7 * j) % 40
+        w[j % 4][b, t, h, j] = BAD[j % 3]
+        hit[b, h] = True
+    g2 = ck.la_bwd_chunked(w[0], w[1], w[2], a, w[3], S0=S0, dS_final=dSf)
+    assert ck.device_status() == 0
+    for n in ("dq", "dk", "dv", "dalpha"):
+        x, y = (u[n].movedim(1, 2)[~hit] for u in (g, g2))
+        assert torch.equal(x, y), n
+        assert torch.isfinite(g[n]).all()
+    assert torch.equal(g["dS0"][~hit], g2["dS0"][~hit])
