@@ -176,7 +176,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     prefetch_tmap(&tm_q);
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
-    if (!SUM) prefetch_tmap(&tm_o);
+    if (!SUM && sizeof(Tout) == 2) prefetch_tmap(&tm_o);  // (fp32 rows are stored by threads)
   }
   if (warp == 0) {
     tmem_alloc(sb + OFF_MISC, kTmemCols);
