@@ -28,6 +28,8 @@
 // segment's own state to its end (keys and values only), the second starts
 // every segment from their decayed sum (backward of B = 2, T = 1000, H = 4,
 // d = 64, fp32, with the decays' gradient: 174 -> 85 us).
+#include <type_traits>
+
 #include "la_common.cuh"
 
 namespace ckda {
@@ -382,7 +384,8 @@ template <int DK, int COLS, typename Tin, typename Tout, bool REV>
 static cudaError_t rec_run(const RecArgs& a, cudaStream_t st) {
   const unsigned n = (unsigned)(a.DV / COLS) * a.H * a.n_seqs;
   if (a.seg_n > 1) {
-    la_rec_kernel<DK, COLS, Tin, Tout, REV, true><<<n * (a.seg_n - 1), kRecThreads, 0, st>>>(a);
+    // (which has no output)
+    la_rec_kernel<DK, COLS, Tin, Tin, REV, true><<<n * (a.seg_n - 1), kRecThreads, 0, st>>>(a);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -392,8 +395,11 @@ static cudaError_t rec_run(const RecArgs& a, cudaStream_t st) {
 
 template <int DK, int COLS, typename Tin, typename Tout>
 static cudaError_t rec_launch(const RecArgs& a, bool rev, cudaStream_t st) {
-  return rev ? rec_run<DK, COLS, Tin, Tout, true>(a, st)
-             : rec_run<DK, COLS, Tin, Tout, false>(a, st);
+  // Backward in time there is one type, and d_k = d_v = 16 runs in la_rec3_kernel.
+  if constexpr (std::is_same<Tin, Tout>::value && DK + COLS > 32) {
+    if (rev) return rec_run<DK, COLS, Tin, Tout, true>(a, st);
+  }
+  return rev ? cudaErrorInvalidValue : rec_run<DK, COLS, Tin, Tout, false>(a, st);
 }
 
 template <int DK, typename Tin, typename Tout>
