@@ -1,5 +1,7 @@
 """Accuracy of head-decay linear attention and of the norm's weight gradients in
-relative 2-norm, per tensor and per head (needs a B200; bounds in la_norms)."""
+relative 2-norm, per tensor and per head (needs a B200; bounds in la_norms),
+and the walks that only larger calls take: many (chunk, head) pairs per block
+of the backward."""
 import pytest
 import torch
 
@@ -49,3 +51,40 @@ def test_accuracy_of_long_sequences(ck, dtype):  # noqa: F811
     ref = la_ref.backward(q, k, v, a, dO)
     ref["dS0"] = None
     check_backward(ck.la_bwd_chunked(q, k, v, a, dO), ref, tc)
+
+
+@pytest.mark.parametrize("dk,dv", [(128, 128), (64, 128), (128, 64), (64, 64)])
+def test_packed_backward_of_many_chunks(ck, dk, dv):  # noqa: F811
+    """More (chunk, head) pairs than blocks: whole and partial chunks and empty slots follow one
+    another in a block.  Every sequence's gradients equal those of a call on it alone."""
+    g = torch.Generator().manual_seed(dk + dv)
+    lens = [0, 400, 1] + torch.randint(0, 400, (37,), generator=g).tolist()
+    lens[10] = lens[11] = 0
+    lens[20], lens[21] = 128, 256
+    cu = torch.tensor([0] + lens, device=DEV).cumsum(0).to(torch.int32)
+    H, n = 8, len(lens)
+    q, k, v, a, dO, S0, dSf = make((sum(lens),), H, dk, dv, torch.bfloat16, seed=21, n=n)
+    got = ck.la_bwd_chunked(q, k, v, a, dO, S0=S0, dS_final=dSf, cu_seqlens=cu)
+    assert ck.device_status() == 0
+    bounds = cu.tolist()
+    for i in range(n):
+        s = slice(bounds[i], bounds[i + 1])
+        part = [x[s][None].contiguous() for x in (q, k, v, a, dO)]
+        one = ck.la_bwd_chunked(*part, S0=S0[i:i + 1], dS_final=dSf[i:i + 1])
+        for x in ("dq", "dk", "dv", "dalpha"):
+            assert torch.equal(got[x][s], one[x][0]), (x, i)
+        assert torch.equal(got["dS0"][i], one["dS0"][0])
+        if i in (1, 2, 5, 20, 39):
+            check_backward({x: got[x][s][None] if x != "dS0" else got[x][i:i + 1] for x in got},
+                           la_ref.backward(*part, S0[i:i + 1], dSf[i:i + 1]), True)
+
+
+def test_backward_repeats_itself(ck):  # noqa: F811
+    q, k, v, a, dO, _, _ = make((2, 1500), 16, 128, 128, torch.bfloat16, seed=22, states=False)
+    o, S = ck.la_fwd_chunked(q, k, v, a)
+    g = ck.la_bwd_chunked(q, k, v, a, dO)
+    for _ in range(5):
+        o2, S2 = ck.la_fwd_chunked(q, k, v, a)
+        g2 = ck.la_bwd_chunked(q, k, v, a, dO)
+        assert torch.equal(o, o2) and torch.equal(S, S2)
+        assert all(torch.equal(g[n], g2[n]) for n in g)
