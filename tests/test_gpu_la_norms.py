@@ -1,12 +1,13 @@
 """Accuracy of head-decay linear attention and of the norm's weight gradients in
 relative 2-norm, per tensor and per head (needs a B200; bounds in la_norms),
 and the walks that only larger calls take: many (chunk, head) pairs per block
-of the backward."""
+of the backward, several units per warp of the norm."""
 import pytest
 import torch
 
 import la_norms
 import la_ref
+import test_gpu_qk_norm as qkn
 from test_gpu_la import DEV, ck, make, tensor_core  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -88,3 +89,24 @@ def test_backward_repeats_itself(ck):  # noqa: F811
         g2 = ck.la_bwd_chunked(q, k, v, a, dO)
         assert torch.equal(o, o2) and torch.equal(S, S2)
         assert all(torch.equal(g[n], g2[n]) for n in g)
+
+
+@pytest.mark.parametrize("n,Hq,Hk,d,rot,dtype,il", [
+    (6000, 20, 4, 128, 128, torch.bfloat16, False),  # two batches of rows, two units per warp
+    (4000, 12, 3, 128, 64, torch.float32, True),
+    (3700, 36, 1, 64, 64, torch.bfloat16, False),
+    (9001, 5, 5, 16, 8, torch.float32, False),
+])
+def test_norm_of_many_tokens(ck, n, Hq, Hk, d, rot, dtype, il):  # noqa: F811
+    args = qkn.make(n, Hq, Hk, d, rot, dtype, seed=n)
+    qkn.check(ck, args, il=il)
+    q, k, gq, gk, c = args
+    g = ck.qk_norm_rope_bwd(q, k, gq, gk, interleaved=il, **c)
+    for x, w, dy, dx, dw in ((q, c["wq"], gq, g["dq"], g["dwq"]),
+                             (k, c["wk"], gk, g["dk"], g["dwk"])):
+        x, w = (t.detach().cpu().double().requires_grad_() for t in (x, w))
+        qkn.ref_fwd(x, w, c, "rms", il).backward(dy.cpu().double())
+        la_norms.check(dw, w.grad, la_norms.DW, "dw")
+        la_norms.check(dx, x.grad, la_norms.ROUND if dtype == torch.bfloat16 else la_norms.DW, "dx", 1)
+    again = ck.qk_norm_rope_bwd(q, k, gq, gk, interleaved=il, **c)
+    assert all(torch.equal(g[x], again[x]) for x in g)
