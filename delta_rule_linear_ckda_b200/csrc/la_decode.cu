@@ -8,10 +8,10 @@
 // be summed over the rows before the state can be written back, so the new
 // state leaves at once and the column sums follow it.
 //
-// A CTA owns CV columns of one (sequence, head): all of them when there are
-// enough heads to fill the GPU, else a slice of them (the columns are
-// independent), so that a single token of one sequence uses four times as
-// many SMs.  The choice and both sides' times stand at launch_la_decode.
+// A CTA owns CV columns of one (sequence, head): all of them or, for few heads
+// of the largest state, 16 (the columns are independent), so that one token
+// of one sequence uses d_v / 16 = 8 times as many SMs.  The choice and both
+// sides' times stand at launch_la_decode.
 #include "la_common.cuh"
 
 namespace ckda {
@@ -127,8 +127,14 @@ cudaError_t launch_la_decode(int dtype, int out_dtype, int dk, int dv, const voi
                              const void* v, const float* alpha, int per_head, float* S, void* out,
                              int B, int H, cudaStream_t stream) {
   const int BH = B * H;
-  // Fewer heads than two per SM: slices of 16 columns.
-  const la::StepArgs p{q, k, v, alpha, per_head, S, out, BH, H, dv, BH < 2 * 148};
+  // Slices of 16 columns for at most half as many heads as SMs with a state of
+  // 64 KB.  us, slices / whole heads, bf16 inputs, one call after another:
+  //   d_k = d_v = 128: 16 heads 2.1 / 2.9, 32: 2.8 / 3.6, 64: 3.9 / 4.0, 80: 4.2 / 4.2,
+  //   128: 5.1 / 4.9, 256: 8.3 / 7.3
+  // Smaller states are not worth it at any number (d_k = 64, d_v = 128: 32 heads
+  // 2.3 / 2.1, 128: 4.0 / 3.4; d_k = 128, d_v = 64: 2.2 / 2.2, 3.9 / 3.4).
+  const la::StepArgs p{q, k, v, alpha, per_head, S, out, BH, H, dv,
+                       dk == 128 && dv == 128 && BH <= 148 / 2};
   if (dtype == CKDA_BF16)
     return out_dtype == CKDA_BF16 ? la::step_rows<__nv_bfloat16, __nv_bfloat16>(dk, p, stream)
                                   : la::step_rows<__nv_bfloat16, float>(dk, p, stream);
