@@ -376,14 +376,22 @@ __global__ void __launch_bounds__(1024) dw_kernel(const float* __restrict__ part
   }
 }
 
-constexpr int kBwdCtas = 148 * 3;  // per side at most, with sums: as many as an SM holds twice
+// CTAs of a side at most, with sums.  us with 1, 2, 3 and 4 per SM, 32768
+// tokens, bf16: 16 query heads of 128 alone 112, 80, 101, 85; 32 + 8 heads of
+// 128 245, 181, 182, 186; 32 + 1 241, 170, 177, 175; 16 + 16 of 64 86, 90, 94,
+// 96; fp32, 16 + 16 of 128 258, 247, 248, 247.
+constexpr int kBwdCtas = 148 * 2;
 
 // Heads of a token that one warp takes: all of them (in up to `most` passes)
-// when the tokens alone give every SM 16 warps, else one pass's.
+// when that leaves every SM three warps of a side, else one pass's.  us with one
+// pass / all heads (16 + 16 of 128, bf16), forward: 148 tokens 3.0 / 3.9,
+// 296: 4.0 / 4.3, 592: 6.4 / 4.8, 1184: 11.2 / 6.4; backward: 6.1 / 8.0,
+// 7.9 / 8.5, 11.8 / 8.9, 19.4 / 11.1; fp32 and 32 + 32 heads change over
+// between 296 and 592 tokens too.
 static void plan(Args* p, int rpw, int most, unsigned cap) {
   for (Side& s : p->s) {
     const int64_t all = p->tokens * ((s.H + most * rpw - 1) / (most * rpw));
-    s.heads_warp = all >= 148 * 16 ? most * rpw : rpw;
+    s.heads_warp = all >= 148 * 3 ? most * rpw : rpw;
     s.units = p->tokens * ((s.H + s.heads_warp - 1) / s.heads_warp);
     const int64_t ctas = (s.units + kWarps - 1) / kWarps;
     s.ctas = cap != 0 && ctas > cap ? cap : (unsigned)ctas;
