@@ -332,17 +332,24 @@ __global__ void __launch_bounds__(kRecThreads, 4) la_rec3_kernel(const Rec3Args 
 constexpr int rec_columns(int dv) { return dv == 16 ? 16 : 32; }
 
 // Segments per sequence of recurrences with `dv` columns that run together:
-// as many as give every SM four CTAs, if each keeps a chunk.  The last segment
-// adds up the states of all others, about 0.8 us each, and a token takes about
-// 0.16 us in the two launches: more than sqrt(T / 5) segments cost more than
-// they give.
+// as many as give every SM four CTAs, if each keeps a chunk, and at most
+// sqrt(T / 2), since the last segment adds up the states of all others.  One
+// head forward, fp32, us with 16 / 32 / 64 / 128 segments:
+//   T = 2048   d = 16: 18 / 18,             64: 30 / 24,             128: 42 / 33
+//   T = 8192   d = 16: 47 / 32 / 28 / 36,   64: 87 / 52 / 42 / 50,   128: 127 / 75 / 70 / 95
+//   T = 32768  d = 16: 161 / 89 / 56 / 49,  64: 316 / 167 / 99 / 90, 128: 469 / 247 / 204 / 212
+// A launch takes as long as its longest segment, so that the count is one which
+// gives them all about the same number of chunks (T = 8192, d = 128: 40 segments
+// of 3 or 4 chunks 99 us, 64 of 2 chunks 70).
 static int rec_segments(int together, int n_seqs, int T, int H, int dv, bool varlen) {
   const int64_t ctas = (int64_t)together * n_seqs * H * (dv / rec_columns(dv));
   const int64_t len = (int64_t)T / (n_seqs > 0 && varlen ? n_seqs : 1);
   int64_t g = 148 * 4 / (ctas > 0 ? ctas : 1);
   if (g > len / kChunk) g = len / kChunk;
-  while (g > 1 && 5 * g * g > len) --g;
-  return g < 2 ? 1 : (int)g;
+  while (g > 1 && 2 * g * g > len) --g;
+  if (g < 2) return 1;
+  const int64_t chunks = (len + kChunk - 1) / kChunk, per = (chunks + g - 1) / g;
+  return (int)((chunks + per - 1) / per);
 }
 
 // Floats of the segments' states and decays.
