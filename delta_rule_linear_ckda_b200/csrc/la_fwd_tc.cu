@@ -702,8 +702,10 @@ static int fwd_segments(int n_seqs, int T, int H, int dv, bool varlen) {
 
 // The first launch leaves the last segment out: smaller pieces fill the SMs.
 // A segment adds up the states of all pieces before it, about 0.7 us each, so
-// that there are no more than eight of them unless the segments alone are more
-// (one head, T = 16384, 16 segments: 98 us with 8 pieces each, 57 with one).
+// that there are no more than eight of them unless the segments alone are more.
+// us with 1 / 2 / 4 / 8 pieces, d = 128: T = 4096, one head, 4 segments 44 / 42 /
+// 46 / 57; T = 16384, one head, 16 segments 57 / 67 / 98 / 168; T = 65536, 32
+// heads, 2 segments 1048 / 851 / 857.
 static int fwd_pieces(int n_seqs, int H, int dv, int segs) {
   if (segs == 1) return 1;
   const int64_t ctas = (int64_t)n_seqs * H * (dv / fw::BV) * (segs - 1);
