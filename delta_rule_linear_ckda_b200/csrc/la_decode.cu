@@ -2,7 +2,8 @@
 //   S <- a S + k v^T,   o = S^T q.
 //
 // The step moves 8 d_k d_v bytes of state per (sequence, head) and does four
-// fp32 operations per element: it is bound by HBM bandwidth.  Each thread
+// fp32 operations per element: it is bound by HBM bandwidth (B = 256, H = 32,
+// d = 128: 160 us, the copy rate; issue slots 17 %).  Each thread
 // owns four adjacent columns (one 16-byte vector) of NR rows and requests
 // them all before it uses one.  Unlike the delta-rule steps nothing has to
 // be summed over the rows before the state can be written back, so the new

@@ -30,7 +30,10 @@
 //
 // Roundings: the scores (after their decays) and the state's copy that the
 // queries read are rounded once to bf16, like the inputs; both only reach
-// out.  The state itself stays at fp32 accuracy: diag(suf) V is split into
+// out, whose error is 2.35e-3 (2-norm) in bf16 where the result's own rounding
+// is 1.66e-3, and 1.66e-3 in fp32.  Second terms have no room: the 512 columns of
+// tensor memory and all but 500 bytes of shared memory are in use.  Inputs in
+// fp32 take the fp32 kernels.  The state itself stays at fp32 accuracy: diag(suf) V is split into
 // three bf16 terms (24 bits) whose products with the exact bf16 K are one MMA
 // with the terms side by side (N = 192): shared memory, whose bandwidth bounds
 // this kernel, is read for K once instead of three times.
@@ -39,8 +42,8 @@
 // not: such values are taken out of V's tile (never out of the state's
 // operand) and the rows from their token on set to NaN, which is what the
 // state, now NaN in that column, gives the later chunks.  Rows before it keep
-// their values.  The check takes 2 % of the time (prefill 90.8 -> 92.6 us), in
-// the conversion or after it behind a barrier of its own alike.
+// their values.  The check costs 1 % (B = 4, T = 4096, H = 16, d = 128: 88.8 ->
+// 89.8 us; on V itself instead of the third terms 91.1).
 //
 // A sequence may be split into segments that run at the same time (few
 // sequences and heads): a first launch computes each segment's own end state
@@ -418,7 +421,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // not wait for the queries' product with the last chunk's state
       const int st = c & 1;
       const int len = len_of(c);
-      uint32_t zero = 0;  // this thread's V times zero: a pair of zeros if all of it is finite
+      uint32_t odd = 0;  // the third terms' bits: NaN for a v that is not finite
       if (!(ok = wait(B_DEC + 8 * st, c >> 1))) break;
       {
         const float4 tot = *reinterpret_cast<const float4*>(tots(c));
@@ -439,10 +442,10 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint32_t in[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
             uint32_t t1[8], t2[8], t3[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              split3(in[e], w2, &t1[e], &t2[e], &t3[e]);
-              if constexpr (!SUM)
-                asm("fma.rn.bf16x2 %0, %1, %2, %0;" : "+r"(zero) : "r"(in[e]), "r"(0));
+            for (int e = 0; e < 8; ++e) split3(in[e], w2, &t1[e], &t2[e], &t3[e]);
+            if constexpr (!SUM) {
+#pragma unroll
+              for (int e = 0; e < 8; e += 2) odd |= t3[e] | t3[e + 1];
             }
             uint8_t* d = sm + OFF_VW;
             *reinterpret_cast<uint4*>(d + o0) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
@@ -474,17 +477,28 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       tc_fence_before();
       arrive(B_VW);
       if constexpr (!SUM) {
-        if (__builtin_expect((zero & 0x7fff7fffu) != 0, 0)) {
+        // (the highest bit of an exponent: set in NaN, and in the third term of a
+        // v of 2^17 or more, which is let through here)
+        if (__builtin_expect((odd & 0x40004000u) != 0, 0)) {
 #pragma unroll 1
-          for (int e = kHalf * hf; e < kHalf * (hf + 1); ++e) {
-            uint16_t* x = reinterpret_cast<uint16_t*>(sm + OFF_V + st * 16384 +
-                                                      sw128_chunk(r, e & ~7, 128)) + (e & 7);
-            if ((*x & 0x7f80) == 0x7f80) {
-              *x = 0;
-              atomicMin(bad_from + e, c * C + r);
-            }
+          for (int e = kHalf * hf; e < kHalf * (hf + 1); e += 8) {
+            uint16_t* x =
+                reinterpret_cast<uint16_t*>(sm + OFF_V + st * 16384 + sw128_chunk(r, e, 128));
+            const uint4 w = *reinterpret_cast<const uint4*>(x);
+            uint32_t zero = 0;  // times zero: a pair of zeros, or NaN
+            asm("fma.rn.bf16x2 %0, %1, %5, %0;\n\tfma.rn.bf16x2 %0, %2, %5, %0;\n\t"
+                "fma.rn.bf16x2 %0, %3, %5, %0;\n\tfma.rn.bf16x2 %0, %4, %5, %0;"
+                : "+r"(zero)
+                : "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w), "r"(0));
+            if ((zero & 0x7fff7fffu) == 0) continue;
+#pragma unroll 1
+            for (int u = 0; u < 8; ++u)
+              if ((x[u] & 0x7f80) == 0x7f80) {
+                x[u] = 0;
+                atomicMin(bad_from + e + u, c * C + r);
+              }
+            *reinterpret_cast<volatile int*>(bad_any) = 1;
           }
-          *reinterpret_cast<volatile int*>(bad_any) = 1;
         }
         // (the old operand has been read)
         if (c > 0 && !(ok = wait(B_QS + 8 * (st ^ 1), (c - 1) >> 1))) break;

@@ -131,3 +131,18 @@ def test_backward_after_and_before_other_chunks(ck):  # noqa: F811
         assert torch.equal(x, y), n
         assert torch.isfinite(g[n]).all()
     assert torch.equal(g["dS0"][~hit], g2["dS0"][~hit])
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_finite_values_pass(ck, dtype):  # noqa: F811
+    """Values far above those of other tests, but finite: a power of two scales every result."""
+    q, k, v, a, dO, S0, dSf = make((2, 300), 2, 128, 64, dtype, "signed", seed=4)
+    o, S = ck.la_fwd_chunked(q, k, v, a, S0=S0)
+    g = ck.la_bwd_chunked(q, k, v, a, dO, S0=S0)
+    f = 2.0 ** 40
+    o2, S2 = ck.la_fwd_chunked(q, k, v * f, a, S0=S0 * f)
+    g2 = ck.la_bwd_chunked(q, k, v * f, a, dO, S0=S0 * f)
+    assert ck.device_status() == 0
+    assert torch.equal(o2, o * f) and torch.equal(S2, S * f)
+    for n, x in (("dq", f), ("dk", f), ("dv", 1.0), ("dalpha", f), ("dS0", 1.0)):
+        assert torch.equal(g2[n], g[n] * x), n
