@@ -100,6 +100,9 @@ int qk_sizes(int64_t tokens, int Hq, int Hk, int d, int rot, int norm, float eps
   const int per16 = dtype == CKDA_BF16 ? 8 : 4;
   if (q_stride % per16 != 0 || k_stride % per16 != 0) return CKDA_ERR_MISALIGNED;
   if (tokens > (int64_t)INT32_MAX || (int64_t)Hq + Hk > 65535) return CKDA_ERR_UNSUPPORTED;
+  // (the rows' extent in bytes stays in 63 bits)
+  const int64_t most = (INT64_MAX >> 4) / (tokens > 0 ? tokens : 1);
+  if (q_stride > most || k_stride > most) return CKDA_ERR_INVALID_ARG;
   return CKDA_OK;
 }
 
