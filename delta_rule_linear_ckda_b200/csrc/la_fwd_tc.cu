@@ -33,10 +33,12 @@
 // out, whose error is 2.35e-3 (2-norm) in bf16 where the result's own rounding
 // is 1.66e-3, and 1.66e-3 in fp32.  Second terms have no room: the 512 columns of
 // tensor memory and all but 500 bytes of shared memory are in use.  Inputs in
-// fp32 take the fp32 kernels.  The state itself stays at fp32 accuracy: diag(suf) V is split into
-// three bf16 terms (24 bits) whose products with the exact bf16 K are one MMA
-// with the terms side by side (N = 192): shared memory, whose bandwidth bounds
-// this kernel, is read for K once instead of three times.
+// fp32 take the fp32 kernels.
+//
+// The state itself stays at fp32 accuracy: diag(suf) V is split into three bf16
+// terms (24 bits) whose products with the exact bf16 K are one MMA with the
+// terms side by side (N = 192): shared memory, whose bandwidth bounds this
+// kernel, is read for K once instead of three times.
 //
 // P is zero right of the diagonal, but zero times a v that is not finite is
 // not: such values are taken out of V's tile (never out of the state's

@@ -15,9 +15,11 @@
 // bytes per row the arithmetic and the angles show, 57 and 61 % of the issue
 // slots with the 16 warps that 106 and 128 registers leave an SM, and a warp
 // has nothing of its next token in flight.  The last reduction of the weights'
-// gradients takes 7 us of the backward.  A thread owns two units of G adjacent channels (G = 8: 16 bytes of bf16) that
-// hold whole pairs, so that the turn needs no exchange between threads; the
-// d / (2 G) threads of a row are adjacent lanes and sum over it by shuffles.
+// gradients takes 7 us of the backward.
+//
+// A thread owns two units of G adjacent channels (G = 8: 16 bytes of bf16)
+// that hold whole pairs, so that the turn needs no exchange between threads;
+// the d / (2 G) threads of a row are adjacent lanes and sum over it by shuffles.
 // A warp takes some of one token's query heads, or key heads, so that a
 // thread computes the sines and cosines of its own pairs once for all of them
 // and no barrier stands between the rows.  It requests several rows per lane
