@@ -90,10 +90,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, float4 v) {
 // thread of the CTA calls it once, before any other use of the barrier.
 // Fixed-length batches (cu == NULL) and very large batches keep z.
 constexpr int kLongestFirstMaxSeqs = 1024;
-__device__ __forceinline__ int seq_longest_first(const int32_t* cu, int n_seqs, int z) {
+// The result passes through `pick` in shared memory.
+__device__ __forceinline__ int seq_longest_first(const int32_t* cu, int n_seqs, int z, int* pick) {
   if (cu == nullptr || n_seqs > kLongestFirstMaxSeqs) return z;
-  __shared__ int pick;
-  if (threadIdx.x == 0) pick = z;
+  if (threadIdx.x == 0) *pick = z;
   __syncthreads();
   for (int n = threadIdx.x; n < n_seqs; n += blockDim.x) {
     const int ln = cu[n + 1] - cu[n];
@@ -102,10 +102,15 @@ __device__ __forceinline__ int seq_longest_first(const int32_t* cu, int n_seqs, 
       const int lm = cu[m + 1] - cu[m];
       rank += (lm > ln || (lm == ln && m < n)) ? 1 : 0;
     }
-    if (rank == z) pick = n;
+    if (rank == z) *pick = n;
   }
   __syncthreads();
-  return pick;
+  return *pick;
+}
+
+__device__ __forceinline__ int seq_longest_first(const int32_t* cu, int n_seqs, int z) {
+  __shared__ int pick;
+  return seq_longest_first(cu, n_seqs, z, &pick);
 }
 
 // Token range of sequence n: fixed-length batches use n*T .. (n+1)*T;

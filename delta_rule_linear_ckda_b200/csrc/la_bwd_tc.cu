@@ -101,7 +101,8 @@ la_states_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant
   const bool rev = b & 1;
   b >>= 1;
   const int h = b % p.H;
-  const int n = longest_first(p.cu, p.n_seqs, b / p.H, reinterpret_cast<int*>(sm + OFF_MISC + 4));
+  const int n =
+      seq_longest_first(p.cu, p.n_seqs, b / p.H, reinterpret_cast<int*>(sm + OFF_MISC + 4));
   const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
   if (!sr.ok) return;
   const uint32_t bar = sb + OFF_BAR;

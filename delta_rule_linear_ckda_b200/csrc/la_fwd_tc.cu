@@ -158,7 +158,7 @@ la_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   b /= nseg;
   const int h = b % p.H;
   int* pick = reinterpret_cast<int*>(sm + OFF_MISC + 4);
-  const int n = longest_first(p.cu, p.n_seqs, b / p.H, pick);
+  const int n = seq_longest_first(p.cu, p.n_seqs, b / p.H, pick);
   const SeqRange sr = seq_range(p.cu, n, p.n_seqs, p.T, p.status);
   if (!sr.ok) return;
 

@@ -12,25 +12,6 @@
 namespace ckda {
 namespace la {
 
-// The sequence of rank z by decreasing length (see seq_longest_first), with
-// the result passed on through `pick` in the caller's shared memory.
-__device__ __forceinline__ int longest_first(const int32_t* cu, int n_seqs, int z, int* pick) {
-  if (cu == nullptr || n_seqs > kLongestFirstMaxSeqs) return z;
-  if (threadIdx.x == 0) *pick = z;
-  __syncthreads();
-  for (int n = threadIdx.x; n < n_seqs; n += blockDim.x) {
-    const int ln = cu[n + 1] - cu[n];
-    int rank = 0;
-    for (int m = 0; m < n_seqs; ++m) {
-      const int lm = cu[m + 1] - cu[m];
-      rank += (lm > ln || (lm == ln && m < n)) ? 1 : 0;
-    }
-    if (rank == z) *pick = n;
-  }
-  __syncthreads();
-  return *pick;
-}
-
 // Products over a warp's lanes: through this lane, and behind it.
 template <typename T>
 __device__ __forceinline__ T warp_prefix(T a, int lane) {
